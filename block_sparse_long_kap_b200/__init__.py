@@ -22,7 +22,9 @@ __all__ = [
     "cosa_kap_select_group", "cosa_osk_attention_group", "cosa_attention_host_workspace_size",
     "cosa_attention_host", "cosa_debug_osk_wait_fault", "cosa_kap_pool", "cosa_kap_rank",
     "cosa_kap_preskip", "cosa_osk_decode", "cosa_osk_decode_workspace_size",
-    "cosa_prefill_write",
+    "cosa_prefill_write", "ChunkShape", "RopeParams", "ScoreParams", "EvictParams",
+    "cosa_chunk_write", "cosa_chunk_attention_workspace_size", "cosa_chunk_attention",
+    "cosa_attention_mass", "cosa_cache_evict",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +36,9 @@ EXPORTED_SYMBOLS = (
     "cosa_dense_attention", "cosa_get_status", "cosa_kap_select_group", "cosa_osk_attention_group",
     "cosa_attention_host_workspace_size", "cosa_attention_host", "cosa_debug_osk_wait_fault",
     "cosa_kap_pool", "cosa_kap_rank", "cosa_kap_preskip", "cosa_osk_decode",
-    "cosa_osk_decode_workspace_size", "cosa_prefill_write",
+    "cosa_osk_decode_workspace_size", "cosa_prefill_write", "cosa_chunk_write",
+    "cosa_chunk_attention_workspace_size", "cosa_chunk_attention", "cosa_attention_mass",
+    "cosa_cache_evict",
 )
 
 # Largest workspace the allocation-free Stage-1 entry point accepts (cosa.h).
@@ -70,6 +74,28 @@ class _Kap(ctypes.Structure):
 
 class _Osk(ctypes.Structure):
     _fields_ = [("eps", ctypes.c_float), ("max_run", ctypes.c_int32)]
+
+
+class _Chunk(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "num_q_heads", "num_kv_heads", "head_dim", "page_size", "total_q",
+                 "max_q", "max_kv", "pages_per_seq", "num_phys_pages")] + \
+               [("softmax_scale", ctypes.c_float)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("interleaved", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
+
+
+class _Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p)]
+
+
+class _Evict(ctypes.Structure):
+    _fields_ = [("budget", ctypes.c_int32), ("sink", ctypes.c_int32), ("recent", ctypes.c_int32)]
 
 
 @dataclasses.dataclass
@@ -123,6 +149,76 @@ class OskParams:
         return _Osk(self.eps, self.max_run)
 
 
+@dataclasses.dataclass
+class ChunkShape:
+    """A ragged batch of new tokens over the paged cache (cosa.h: cosa_chunk_t)."""
+    batch: int
+    num_q_heads: int
+    num_kv_heads: int
+    head_dim: int
+    page_size: int
+    total_q: int                # rows of the token-major tensors
+    max_q: int                  # bound on a sequence's new tokens
+    max_kv: int                 # bound on a sequence's keys, the new ones included
+    pages_per_seq: int = 0      # 0 -> ceil(max_kv / page_size)
+    num_phys_pages: int = 0     # 0 -> batch * pages_per_seq
+    softmax_scale: float = 0.0  # 0 -> 1/sqrt(head_dim)
+
+    def c(self) -> _Chunk:
+        pps = self.pages_per_seq or -(-self.max_kv // max(self.page_size, 1))
+        nphys = self.num_phys_pages or self.batch * pps
+        scale = self.softmax_scale or 1.0 / math.sqrt(max(self.head_dim, 1))
+        return _Chunk(self.batch, self.num_q_heads, self.num_kv_heads, self.head_dim,
+                      self.page_size, self.total_q, self.max_q, self.max_kv, pps, nphys, scale)
+
+
+@dataclasses.dataclass
+class RopeParams:
+    """Rotary positions: pairs of each axis and their order (cosa.h: cosa_rope_params_t)."""
+    sections: tuple = ()
+    interleaved: bool = False
+    adjacent: bool = False
+
+    def c(self) -> _Rope:
+        if len(self.sections) > 4:
+            raise ValueError("at most 4 rotary axes")
+        sec = (ctypes.c_int32 * 4)(*self.sections)
+        return _Rope(len(self.sections), sec, int(bool(self.interleaved)), int(bool(self.adjacent)))
+
+
+@dataclasses.dataclass
+class ScoreParams:
+    """Shape of the scores and mask (cosa.h: cosa_score_params_t); the tensors are device
+    tensors or None."""
+    softcap: float = 0.0
+    window: int = 0
+    slopes: Optional[object] = None       # fp32 [H_q]
+    first_key: Optional[object] = None    # int32 [total_q]
+    prefix_len: Optional[object] = None   # int32 [B]
+
+    def c(self, s: _Chunk, dev: int) -> _Score:
+        import torch
+        if self.slopes is not None:
+            _arg(self.slopes, "slopes", torch.float32, (s.num_q_heads,), dev)
+        if self.first_key is not None:
+            _arg(self.first_key, "first_key", torch.int32, (s.total_q,), dev)
+        if self.prefix_len is not None:
+            _arg(self.prefix_len, "prefix_len", torch.int32, (s.batch,), dev)
+        return _Score(self.softcap, self.window, _ptr(self.slopes), _ptr(self.first_key),
+                      _ptr(self.prefix_len))
+
+
+@dataclasses.dataclass
+class EvictParams:
+    """What an eviction keeps (cosa.h: cosa_evict_params_t)."""
+    budget: int
+    sink: int = 0
+    recent: int = 0
+
+    def c(self) -> _Evict:
+        return _Evict(self.budget, self.sink, self.recent)
+
+
 _lib = None
 
 
@@ -164,6 +260,15 @@ def lib():
     L.cosa_prefill_write.argtypes = [P(_Shape), P(_Kap), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.cosa_kap_preskip.argtypes = [P(_Shape), P(_Kap), ctypes.c_float, ctypes.c_float, vp, vp, vp,
                                    vp, sz, vp]
+    i64 = ctypes.c_int64
+    L.cosa_chunk_write.argtypes = [P(_Chunk), P(_Rope), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                   vp, vp, i64, vp, vp, vp]
+    L.cosa_chunk_attention_workspace_size.argtypes = [P(_Chunk), P(sz)]
+    L.cosa_chunk_attention.argtypes = [P(_Chunk), P(_Score), vp, i64, vp, vp, vp, vp, vp, vp, vp,
+                                       vp, sz, vp]
+    L.cosa_attention_mass.argtypes = [P(_Chunk), P(_Score), vp, i64, vp, vp, vp, vp, vp, i32,
+                                      ctypes.c_float, vp, vp]
+    L.cosa_cache_evict.argtypes = [P(_Chunk), P(_Evict), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in EXPORTED_SYMBOLS:
         if name not in ("cosa_status_string", "cosa_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -574,3 +679,159 @@ def cosa_debug_osk_wait_fault(withhold_k_group: int, wait_limit_ns: int = 0) -> 
 def cosa_get_status(stream=None) -> int:
     """Read and clear the device status word (0 = ok); synchronises the stream."""
     return lib().cosa_get_status(_stream(stream))
+
+
+def _arg(t, name, dtype, shape, dev):
+    """A dense tensor on the current device."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+
+
+def _rows(t, name, shape, dev) -> int:
+    """A token-major bf16 tensor whose rows may be strided (a view of a fused projection);
+    returns the row stride in elements."""
+    import torch
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, h, d = shape
+    st = t.stride()
+    if (st[2] != 1) or (h > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+    return st[0] if n > 1 else h * d
+
+
+def _chunk_cache(s: _Chunk, k_pool, v_pool, page_table, dev) -> None:
+    import torch
+    pool = (s.num_phys_pages, s.num_kv_heads, s.page_size, s.head_dim)
+    _arg(k_pool, "k_pool", torch.bfloat16, pool, dev)
+    if v_pool is not None:
+        _arg(v_pool, "v_pool", torch.bfloat16, pool, dev)
+    _arg(page_table, "page_table", torch.int32, (s.batch, s.pages_per_seq), dev)
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def cosa_chunk_write(shape: ChunkShape, rope: Optional[RopeParams], q_tok, k_tok, v_tok, positions,
+                     inv_freq, cu_q, kv_len, page_table, q, k_pool, v_pool, stream=None) -> None:
+    """Rotate the new tokens' Q and K (positions int32 [axes][total_q], inv_freq fp32 [pairs];
+    rope None or without sections: no rotation) and write Q token-major and K, V behind each
+    sequence's keys in the paged cache.  q_tok [total_q][H_q][D], k_tok / v_tok
+    [total_q][H_kv][D] may be views of a fused projection; q may be q_tok."""
+    import torch
+    s, dev = shape.c(), _current_device()
+    r = None
+    if rope is not None and len(rope.sections):
+        r = rope.c()
+        _arg(positions, "positions", torch.int32, (r.axes, s.total_q), dev)
+        _arg(inv_freq, "inv_freq", torch.float32, (sum(rope.sections),), dev)
+    hq, hk = (s.total_q, s.num_q_heads, s.head_dim), (s.total_q, s.num_kv_heads, s.head_dim)
+    sq, sk, sv = (_rows(q_tok, "q_tok", hq, dev), _rows(k_tok, "k_tok", hk, dev),
+                  _rows(v_tok, "v_tok", hk, dev))
+    so = _rows(q, "q", hq, dev)
+    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
+    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
+    if v_pool is None:
+        raise ValueError("v_pool is required")
+    _chunk_cache(s, k_pool, v_pool, page_table, dev)
+    _check(lib().cosa_chunk_write(
+        ctypes.byref(s), None if r is None else ctypes.byref(r), _ptr(q_tok), sq, _ptr(k_tok), sk,
+        _ptr(v_tok), sv, None if r is None else _ptr(positions), None if r is None else _ptr(inv_freq),
+        _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(q), so, _ptr(k_pool), _ptr(v_pool),
+        _stream(stream)), "cosa_chunk_write")
+
+
+def cosa_chunk_attention_workspace_size(shape: ChunkShape) -> int:
+    out = ctypes.c_size_t(0)
+    s = shape.c()
+    _check(lib().cosa_chunk_attention_workspace_size(ctypes.byref(s), ctypes.byref(out)),
+           "cosa_chunk_attention_workspace_size")
+    return out.value
+
+
+def cosa_chunk_attention(shape: ChunkShape, q, k_pool, v_pool, page_table, cu_q, kv_len, out,
+                         workspace, score: Optional[ScoreParams] = None, lse=None,
+                         stream=None) -> None:
+    """Exact attention of every sequence's new tokens (q [total_q][H_q][D]) over its cache,
+    with the score shaped and masked by `score` (None: plain causal)."""
+    import torch
+    s, dev = shape.c(), _current_device()
+    hq = (s.total_q, s.num_q_heads, s.head_dim)
+    sq = _rows(q, "q", hq, dev)
+    if v_pool is None:
+        raise ValueError("v_pool is required")
+    _chunk_cache(s, k_pool, v_pool, page_table, dev)
+    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
+    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
+    _arg(out, "out", torch.bfloat16, hq, dev)
+    if lse is not None:
+        _arg(lse, "lse", torch.float32, hq[:2], dev)
+    if workspace is None or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
+    sc = None if score is None else score.c(s, dev)
+    _check(lib().cosa_chunk_attention(
+        ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
+        _ptr(v_pool), _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        "cosa_chunk_attention")
+
+
+def cosa_attention_mass(shape: ChunkShape, q, k_pool, page_table, cu_q, kv_len, lse, mass,
+                        score: Optional[ScoreParams] = None, last_q: int = 0, decay: float = 1.0,
+                        stream=None) -> None:
+    """Add the attention weights of the call that left `lse` to the cached keys' mass
+    ([B][H_kv][pages_per_seq * P], in place): those of each sequence's last last_q new tokens
+    (0: all), summed over the heads of the group; old masses are first multiplied by decay."""
+    import torch
+    s, dev = shape.c(), _current_device()
+    sq = _rows(q, "q", (s.total_q, s.num_q_heads, s.head_dim), dev)
+    _chunk_cache(s, k_pool, None, page_table, dev)
+    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
+    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
+    _arg(lse, "lse", torch.float32, (s.total_q, s.num_q_heads), dev)
+    _arg(mass, "mass", torch.float32, (s.batch, s.num_kv_heads, s.pages_per_seq * s.page_size), dev)
+    sc = None if score is None else score.c(s, dev)
+    _check(lib().cosa_attention_mass(
+        ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
+        _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(lse), int(last_q), float(decay),
+        _ptr(mass), _stream(stream)), "cosa_attention_mass")
+
+
+def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page_table, kv_len, mass,
+                     dst_table, kept, new_len, mass_out=None, stream=None) -> None:
+    """Cut every sequence's cache to evict.budget keys a KV head (sink, recent and the heaviest
+    others): their positions to kept [B][H_kv][budget] (ascending, -1 past the end), their K, V
+    and mass to the pages of dst_table [B][ceil(budget / P)], the new lengths to new_len."""
+    import torch
+    s, e, dev = shape.c(), evict.c(), _current_device()
+    if v_pool is None:
+        raise ValueError("v_pool is required")
+    _chunk_cache(s, k_pool, v_pool, page_table, dev)
+    pages = -(-e.budget // s.page_size)
+    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
+    _arg(mass, "mass", torch.float32, (s.batch, s.num_kv_heads, s.pages_per_seq * s.page_size), dev)
+    _arg(dst_table, "dst_table", torch.int32, (s.batch, pages), dev)
+    _arg(kept, "kept", torch.int32, (s.batch, s.num_kv_heads, e.budget), dev)
+    _arg(new_len, "new_len", torch.int32, (s.batch,), dev)
+    if mass_out is not None:
+        _arg(mass_out, "mass_out", torch.float32, (s.batch, s.num_kv_heads, pages * s.page_size), dev)
+    _check(lib().cosa_cache_evict(
+        ctypes.byref(s), ctypes.byref(e), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
+        _ptr(kv_len), _ptr(mass), _ptr(dst_table), _ptr(kept), _ptr(new_len), _ptr(mass_out),
+        _stream(stream)), "cosa_cache_evict")

@@ -1,0 +1,800 @@
+// Attention of a ragged batch of new tokens over the paged cache (cosa_chunk_attention),
+// from one token a sequence to whole prompts, on the sm_100a tensor cores.
+//
+// A tile is 128 rows of (token, query head of the KV head's group): G heads share every
+// K / V block whatever the number of tokens, so a decode step reads the cache once a KV
+// head.  Sequences with more than 128 rows take tiles in pairs (NT = 2), which halves the
+// K / V traffic from L2 and keeps the tensor core on one tile while the other is in its
+// softmax; a step with at most 128 rows a sequence runs one tile (NT = 1) with two S
+// buffers, whose QK^T of the next block runs under the softmax of this one.
+//
+// The work is cut by blocks of 128 keys, not by tiles: chunk_plan_kernel lists every
+// tile's block range [jb, jb + nb) (window, documents and prefix shrink it) and the running
+// sum of nb; the 148 CTAs of chunk_attn_kernel (one per SM, each resident for the whole
+// launch) take equal shares of that sum, a share running over the end of one tile into the
+// next.  A tile cut between CTAs leaves unnormalised fp32 partial rows (at most two a CTA),
+// which chunk_combine_kernel joins; so one long sequence, a ragged batch and a prompt
+// whose tile count does not divide by 148 all end together.
+//
+// Roles of the 4 + 4 NT warps:
+//   warp 0     Q and K loads (TMA through the page table, lane t takes page t)
+//   warp 1     MMA issue (one thread)
+//   warp 2     V loads; values behind the sequence's end are zeroed (they may hold NaN,
+//              and a zero weight times NaN is NaN)
+//   warp 3     TMEM allocation
+//   warps 4..  softmax of tile 0 / 1, one row per thread (its TMEM lane)
+// S, P (bf16, over S) and O live in TMEM; the exponent base m_ref moves only when the row
+// max passes it by 2^8.  Row max, sums and O are fp32; P is rounded to bf16 for the second
+// product (relative error 2^-9 a weight, averaged over the keys), its sum is not.
+// Every wait is bounded, as in the dense kernel.
+#pragma once
+
+#include <type_traits>
+
+#include "chunk_common.cuh"
+
+namespace cosa {
+
+// one tile (pair) of the plan
+struct ChunkTile {
+  int tok0;  // first row of q
+  int ntok;
+  int pos0;  // cache position of that token
+  int b;
+  int jb, nb;  // key blocks, nb >= 1
+  int kv;
+  int prefix;
+};
+static_assert(sizeof(ChunkTile) == 32, "read as two 16-byte words");
+
+// one row of the join list: the CTA whose share starts a tile that it does not finish
+struct ChunkJoin {
+  int ntok;  // 0: none
+  int tok0, hk, pad0;
+  int last;  // the CTA that finishes it
+  int pad1[3];
+};
+
+struct ChunkAttnParams {
+  ChunkSeqs seqs;
+  ChunkMask mask;
+  const int32_t* page_table;
+  const float* slopes;  // [H_q] or null
+  __nv_bfloat16* out;   // [total_q][H_q][D]
+  float* lse;           // [total_q][H_q] or null
+  ChunkTile* tiles;     // workspace [max tiles]
+  long long* cum;       // workspace [max tiles + 1]
+  int* n_tiles;         // workspace
+  ChunkJoin* joins;     // workspace [NUM_SMS]
+  float* part_o;        // workspace [2 NUM_SMS][part_rows][D]
+  float2* part_ml;      // workspace [2 NUM_SMS][part_rows]: exponent base, sum
+  int num_q_heads, num_kv_heads, group, page_size, pages_per_seq, num_phys_pages;
+  int tile_tokens;  // 128 / G
+  int nt;           // tiles a CTA works on at once
+  int part_rows;
+  int max_tiles;    // room in the workspace
+  ScoreShape score;
+  unsigned long long timeout_ns;
+};
+
+// ---- plan -----------------------------------------------------------------------------
+constexpr int PLAN_THREADS = 1024;
+
+__device__ __forceinline__ long long plan_scan(long long v, long long* red, long long& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  long long w = lane < PLAN_THREADS / 32 ? red[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const long long before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  __syncthreads();
+  return (warp ? before : 0) + inc - v;
+}
+
+// One CTA.  Dynamic shared memory: first tile of each sequence, [batch + 1] int.
+__global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkAttnParams p) {
+  extern __shared__ int first_tile[];
+  __shared__ long long red[32];
+  pdl_launch();
+  const int tid = threadIdx.x, B = p.seqs.batch;
+  const int span = p.tile_tokens * p.nt;  // tokens a tile (pair)
+  long long base = 0, total;
+  for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
+    const int b = b0 + tid;
+    long long n = 0;
+    if (b < B) n = (chunk_seq(p.seqs, b).q_len + span - 1) / span;
+    const long long before = plan_scan(n, red, total);
+    if (b < B) first_tile[b] = (int)(base + before);
+    base += total;
+  }
+  // overlapping sequences (cu_q going back and forth) can add up to more tiles than
+  // total_q tokens give: nothing is run then
+  if (base > p.max_tiles && tid == 0) set_status(COSA_ERR_INVALID_ARG);
+  const int T = base > p.max_tiles ? 0 : (int)base;
+  if (tid == 0) {
+    first_tile[B] = T;
+    *p.n_tiles = T;
+  }
+  __syncthreads();
+  base = 0;
+  for (int t0 = 0; t0 < T; t0 += PLAN_THREADS) {
+    const int t = t0 + tid;
+    ChunkTile d;
+    d.nb = 0;
+    if (t < T) {
+      int lo = 0, hi = B - 1;  // the last sequence whose first tile is at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_tile[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const ChunkSeq s = chunk_seq(p.seqs, lo);
+      const int i0 = (t - first_tile[lo]) * span;
+      d.b = lo;
+      d.tok0 = s.q0 + i0;
+      d.ntok = min(span, s.q_len - i0);
+      d.pos0 = s.kv - s.q_len + i0;
+      d.kv = s.kv;
+      d.prefix = p.mask.prefix_len ? __ldg(p.mask.prefix_len + lo) : 0;
+      int kmin = INT_MAX, kmax = -1;
+      if (p.mask.first_key) {
+        for (int i = 0; i < d.ntok; ++i) {
+          int a, z;
+          token_range(p.mask, d.tok0 + i, d.pos0 + i, d.kv, d.prefix, a, z);
+          if (a <= z) {
+            kmin = min(kmin, a);
+            kmax = max(kmax, z);
+          }
+        }
+      } else {  // both ends grow with the position
+        int z;
+        token_range(p.mask, d.tok0, d.pos0, d.kv, d.prefix, kmin, z);
+        int a;
+        token_range(p.mask, d.tok0 + d.ntok - 1, d.pos0 + d.ntok - 1, d.kv, d.prefix, a, kmax);
+      }
+      // a tile without any visible key works through one masked block: zeros and -inf
+      d.jb = kmax >= 0 ? kmin >> 7 : 0;
+      d.nb = kmax >= 0 ? (kmax >> 7) + 1 - d.jb : 1;
+    }
+    const long long before = plan_scan(d.nb, red, total);
+    if (t < T) {
+      p.tiles[t] = d;
+      p.cum[t] = base + before;
+    }
+    base += total;
+  }
+  if (tid == 0) p.cum[T] = base;
+}
+
+// ---- attention ------------------------------------------------------------------------
+template <int D, int NT>
+struct ChunkCfg {
+  static constexpr int KB = 128;                    // keys a block
+  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr uint32_t Q_BYTES = 128 * D * 2;  // one tile
+  static constexpr uint32_t BLK_BYTES = KB * D * 2;
+  static constexpr int KS = D == 128 ? 3 : 5;       // K ring slots
+  static constexpr int VS = D == 128 ? (NT == 1 ? 3 : 2) : 5;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + NT * Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + KS * BLK_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_V + VS * BLK_BYTES;
+  // q full / empty, k full / empty, v full / empty, v tail, s full[2], p full[2],
+  // o full[2], pv done, done
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 6 + 2;
+  static constexpr uint32_t OFF_MISC = (OFF_BAR + NBAR * 8 + 15) & ~15u;
+  static constexpr uint32_t SMEM = OFF_MISC + 32;   // TMEM address, abort, start tile
+  static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
+  static constexpr int COL_O = 256;                 // S buffers at 0 and 128
+  static constexpr float kRescale = 8.0f;
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+// A CTA's walk over its share [w, w_end) of the plan; every role walks by itself.
+struct ChunkWalk {
+  long long w, w_end, per_head;
+  int hk, t, n_tiles;
+  // the segment
+  ChunkTile tile;
+  int jb, nb;       // its blocks
+  int part;         // -1: the whole tile; else partial slot 0 (starts inside) / 1
+  __device__ __forceinline__ bool next(const ChunkTile* tiles, const long long* cum) {
+    if (w >= w_end) return false;
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(tiles + t));
+    const int4 y = __ldcg(reinterpret_cast<const int4*>(tiles + t) + 1);
+    const long long start = hk * per_head + __ldcg(cum + t);
+    tile.tok0 = x.x; tile.ntok = x.y; tile.pos0 = x.z; tile.b = x.w;
+    tile.jb = y.x; tile.nb = y.y; tile.kv = y.z; tile.prefix = y.w;
+    const int off = (int)(w - start);
+    jb = tile.jb + off;
+    const long long left = w_end - w;
+    nb = left < tile.nb - off ? (int)left : tile.nb - off;
+    part = off > 0 ? 0 : (nb < tile.nb ? 1 : -1);
+    return true;
+  }
+  __device__ __forceinline__ void advance() {
+    w += nb;
+    if (jb + nb == tile.jb + tile.nb && ++t == n_tiles) {
+      t = 0;
+      ++hk;
+    }
+  }
+};
+
+template <int D, int NT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(128 + 128 * NT, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const ChunkAttnParams prm) {
+  using C = ChunkCfg<D, NT>;
+  using namespace tc;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+  const uint32_t sb0 = (sraw + 1023u) & ~1023u;
+  uint8_t* sg = smem_raw + (sb0 - sraw);
+  const uint32_t sQ = sb0 + C::OFF_Q, sK = sb0 + C::OFF_K, sV = sb0 + C::OFF_V;
+  const uint32_t bar = sb0 + C::OFF_BAR;
+  const uint32_t b_qfull = bar, b_qempty = bar + 8;
+  auto b_kfull = [&](int s) { return bar + 8u * (2 + s); };
+  auto b_kempty = [&](int s) { return bar + 8u * (2 + C::KS + s); };
+  auto b_vfull = [&](int s) { return bar + 8u * (2 + 2 * C::KS + s); };
+  auto b_vempty = [&](int s) { return bar + 8u * (2 + 2 * C::KS + C::VS + s); };
+  constexpr int B0 = 2 + 2 * C::KS + 2 * C::VS;
+  const uint32_t b_vtail = bar + 8u * B0;
+  auto b_sfull = [&](int i) { return bar + 8u * (B0 + 1 + i); };
+  auto b_pfull = [&](int i) { return bar + 8u * (B0 + 3 + i); };
+  auto b_ofull = [&](int i) { return bar + 8u * (B0 + 5 + i); };
+  const uint32_t b_pv = bar + 8u * (B0 + 7), b_done = bar + 8u * (B0 + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sg + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 4);
+  volatile int* start_tile = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) return;
+  const int G = prm.group, TOK = prm.tile_tokens, P = prm.page_size;
+
+  if (tid == 0) {
+    mbar_init(b_qfull, 1);
+    mbar_init(b_qempty, 1);
+    for (int s = 0; s < C::KS; ++s) { mbar_init(b_kfull(s), 1); mbar_init(b_kempty(s), 1); }
+    for (int s = 0; s < C::VS; ++s) { mbar_init(b_vfull(s), 1); mbar_init(b_vempty(s), 1); }
+    mbar_init(b_vtail, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_sfull(i), 1);
+      mbar_init(b_pfull(i), 4);
+      mbar_init(b_ofull(i), 1);
+    }
+    mbar_init(b_pv, 1);
+    mbar_init(b_done, 1);
+    *abort_flag = 0;
+    *start_tile = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 3) {
+    tmem_alloc(sb0 + C::OFF_MISC, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // ---- this CTA's share of the plan
+  pdl_wait();
+  ChunkWalk walk;
+  walk.n_tiles = __ldcg(prm.n_tiles);
+  walk.per_head = __ldcg(prm.cum + walk.n_tiles);
+  const long long total = walk.per_head * prm.num_kv_heads;
+  const long long quota = (total + gridDim.x - 1) / gridDim.x;
+  walk.w = min((long long)blockIdx.x * quota, total);
+  walk.w_end = min(walk.w + quota, total);
+  walk.hk = 0;
+  walk.t = 0;
+  if (walk.w < walk.w_end) {
+    walk.hk = (int)(walk.w / walk.per_head);
+    const long long rem = walk.w - walk.hk * walk.per_head;
+    for (int t = tid; t < walk.n_tiles; t += C::THREADS)
+      if (__ldcg(prm.cum + t) <= rem && rem < __ldcg(prm.cum + t + 1)) *start_tile = t;
+  }
+  __syncthreads();
+  walk.t = *start_tile;
+
+  const unsigned long long tmo = prm.timeout_ns;
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    set_status(COSA_ERR_TIMEOUT);
+  };
+  // bounded wait on an mbarrier phase; false on timeout or abort
+  auto wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar_addr, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar_addr, parity)) {
+      if (*abort_flag) return false;
+      if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || globaltimer_ns() - t0 > tmo) {
+        give_up();
+        return false;
+      }
+    }
+    return true;
+  };
+  auto wait_warp = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+    int okl = 1;
+    if (lane == 0) okl = wait(bar_addr, parity) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, okl, 0) != 0;
+  };
+  // the same without suspending: for the hand-offs on the softmax / MMA cycle
+  auto wait_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+    if (mbar_test_wait(bar_addr, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t n = 0;
+    while (!mbar_test_wait(bar_addr, parity)) {
+      if ((++n & 255u) == 0) {
+        if (*abort_flag) return false;
+        if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || globaltimer_ns() - t0 > tmo) {
+          give_up();
+          return false;
+        }
+      }
+    }
+    return true;
+  };
+  auto wait_warp_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+    int okl = 1;
+    if (lane == 0) okl = wait_hot(bar_addr, parity) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, okl, 0) != 0;
+  };
+  const int ppb = C::KB / P;  // pages a block, at most 8: one a lane
+  // coordinate of page `lane` of block j (-1: outside the pool, read as zeros)
+  auto page_coord = [&](int b, int hk, int j, int np) -> int {
+    if (lane >= np) return 0;
+    const int ph = __ldg(prm.page_table + (long long)b * prm.pages_per_seq + j * ppb + lane);
+    if (ph < 0 || ph >= prm.num_phys_pages) {
+      set_status(COSA_ERR_INVALID_ARG);
+      return -1;
+    }
+    return ph * prm.num_kv_heads + hk;
+  };
+  auto blk_pages = [&](int kv, int j) { return min(ppb, (kv - j * C::KB + P - 1) / P); };
+
+  if (warp == 0) {
+    // ================= Q and K ========================================================
+    int it = 0, seg = 0;
+    bool ok = true;
+    const int qtok_bytes = G * TOK * 128 * (D / 64);
+    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance(), ++seg) {
+      const int nt = (NT == 2 && walk.tile.ntok > TOK) ? 2 : 1;
+      if (seg > 0 && !wait_warp(b_qempty, (seg - 1) & 1)) { ok = false; break; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(b_qfull, (uint32_t)(nt * qtok_bytes));
+        for (int i = 0; i < nt; ++i)
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(sQ + i * C::Q_BYTES + kb * (128 * 128), &tm_q, b_qfull, kb * 64,
+                        walk.hk * G, walk.tile.tok0 + i * TOK);
+      }
+      int cz = page_coord(walk.tile.b, walk.hk, walk.jb, blk_pages(walk.tile.kv, walk.jb));
+      for (int j = 0; j < walk.nb; ++j, ++it) {
+        const int s = it % C::KS, np = blk_pages(walk.tile.kv, walk.jb + j);
+        int cz_next = 0;
+        if (j + 1 < walk.nb)
+          cz_next = page_coord(walk.tile.b, walk.hk, walk.jb + j + 1,
+                               blk_pages(walk.tile.kv, walk.jb + j + 1));
+        if (it >= C::KS && !wait_warp(b_kempty(s), ((it / C::KS) - 1) & 1)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(b_kfull(s), (uint32_t)(np * P * D * 2));
+        __syncwarp();
+        if (lane < np)
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(sK + s * C::BLK_BYTES + kb * (C::KB * 128) + lane * (P * 128), &tm_k,
+                        b_kfull(s), kb * 64, 0, cz);
+        cz = cz_next;
+      }
+      if (!ok) { ++seg; break; }
+    }
+    // loads never consumed (abort only) land before the CTA leaves
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      if (seg > 0) drain_wait(b_qfull, (seg - 1) & 1, t0, tmo);
+      for (int x = max(0, it - C::KS); x < it; ++x)
+        drain_wait(b_kfull(x % C::KS), (x / C::KS) & 1, t0, tmo);
+    }
+  } else if (warp == 2) {
+    // ================= V ==============================================================
+    int it = 0, tails = 0;
+    bool ok = true;
+    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance()) {
+      int cz = page_coord(walk.tile.b, walk.hk, walk.jb, blk_pages(walk.tile.kv, walk.jb));
+      for (int j = 0; j < walk.nb; ++j, ++it) {
+        const int s = it % C::VS, np = blk_pages(walk.tile.kv, walk.jb + j);
+        const int keys = walk.tile.kv - (walk.jb + j) * C::KB;
+        int cz_next = 0;
+        if (j + 1 < walk.nb)
+          cz_next = page_coord(walk.tile.b, walk.hk, walk.jb + j + 1,
+                               blk_pages(walk.tile.kv, walk.jb + j + 1));
+        if (it >= C::VS && !wait_warp(b_vempty(s), ((it / C::VS) - 1) & 1)) { ok = false; break; }
+        // the MMA reads the keys of whole 16-key steps: those behind the end are zeroed
+        const bool tail = keys < C::KB && (keys & 15) != 0;
+        const uint32_t full = tail ? b_vtail : b_vfull(s);
+        const uint32_t dst = sV + s * C::BLK_BYTES;
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(np * P * D * 2));
+        __syncwarp();
+        if (lane < np)
+#pragma unroll
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(dst + kb * (C::KB * 128) + lane * (P * 128), &tm_v, full, kb * 64, 0, cz);
+        cz = cz_next;
+        if (tail) {
+          // (on a timeout here the slot is reported full all the same: the MMA thread leaves
+          // through the abort flag)
+          const bool have = wait_warp(b_vtail, tails & 1);
+          ++tails;
+          const int nz = 16 - (keys & 15);
+          for (int x = lane; have && x < nz * 8 * (D / 64); x += 32) {
+            const int c = x & 7, r = keys + (x >> 3) % nz, kb = (x >> 3) / nz;
+            st_shared_v4(dst + kb * (C::KB * 128) + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_vfull(s));
+          if (!have) { ++it; ok = false; break; }
+        }
+      }
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      for (int x = max(0, it - C::VS); x < it; ++x)
+        drain_wait(b_vfull(x % C::VS), (x / C::VS) & 1, t0, tmo);
+      if (tails > 0) drain_wait(b_vtail, (tails - 1) & 1, t0, tmo);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ================= MMA issue ====================================================
+      constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, 0);
+      constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, 1);
+      const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sK, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sV, C::KB * 128, 1024);
+      // S buffer sb = Q tile i of this segment times the K block in slot s
+      auto qk = [&](int i, int sbuf, int s) {
+        const uint64_t dqi = dq + ((uint32_t)i * C::Q_BYTES >> 4);
+        const uint64_t dks = dk + ((uint32_t)s * C::BLK_BYTES >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16_ss(tmem + sbuf * 128, dqi + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                      dks + (((k >> 2) * (C::KB * 128) + (k & 3) * 32) >> 4), ID_QK,
+                      k > 0 ? 1u : 0u);
+        mma_commit(b_sfull(sbuf));
+      };
+      // O of tile i (+)= P in S buffer sbuf times the V block in slot s
+      auto pv = [&](int i, int sbuf, int s, int keys, bool first) {
+        const uint64_t dvs = dv + ((uint32_t)s * C::BLK_BYTES >> 4);
+        const int nk = min(C::KB, (keys + 15) & ~15) / 16;
+        for (int k = 0; k < nk; ++k)
+          mma_bf16_ts(tmem + C::COL_O + i * D, tmem + sbuf * 128 + k * 8, dvs + ((k * 16 * 128) >> 4),
+                      ID_PV, (!first || k > 0) ? 1u : 0u);
+      };
+      int it = 0, seg = 0, np[2] = {0, 0};  // blocks, segments, P hand-offs of each tile
+      bool ok = true;
+      for (; ok && walk.next(prm.tiles, prm.cum); walk.advance(), ++seg) {
+        const int nt = (NT == 2 && walk.tile.ntok > TOK) ? 2 : 1, nb = walk.nb;
+        auto keys = [&](int j) { return walk.tile.kv - (walk.jb + j) * C::KB; };
+        auto kslot_wait = [&](int x) { return wait(b_kfull(x % C::KS), (x / C::KS) & 1); };
+        if (!wait(b_qfull, seg & 1) || !kslot_wait(it)) { ok = false; break; }
+        tc_fence_after();
+        for (int i = 0; i < nt; ++i) qk(i, NT == 1 ? it & 1 : i, it % C::KS);
+        mma_commit(b_kempty(it % C::KS));
+        if (nb == 1) mma_commit(b_qempty);
+        for (int j = 0; j < nb; ++j, ++it) {
+          const int vs = it % C::VS;
+          if (NT == 1 && j + 1 < nb) {  // the next block's scores, under this block's softmax
+            if (!kslot_wait(it + 1)) { ok = false; break; }
+            tc_fence_after();
+            qk(0, (it + 1) & 1, (it + 1) % C::KS);
+            mma_commit(b_kempty((it + 1) % C::KS));
+            if (j + 2 == nb) mma_commit(b_qempty);
+          }
+          if (!wait(b_vfull(vs), (it / C::VS) & 1)) { ok = false; break; }
+          bool k_next = false;
+          for (int i = 0; i < nt; ++i) {
+            if (!wait_hot(NT == 1 ? b_pfull(it & 1) : b_pfull(i), (NT == 1 ? it >> 1 : np[i]) & 1)) {
+              ok = false;
+              break;
+            }
+            ++np[i];
+            tc_fence_after();
+            pv(i, NT == 1 ? it & 1 : i, vs, keys(j), j == 0);
+            if (NT == 1) {
+              mma_commit(b_pv);
+              if (j + 1 == nb) mma_commit(b_ofull(0));
+            } else if (j + 1 < nb) {
+              if (!k_next) {
+                if (!kslot_wait(it + 1)) { ok = false; break; }
+                tc_fence_after();
+                k_next = true;
+              }
+              qk(i, i, (it + 1) % C::KS);
+              if (i + 1 == nt) {
+                mma_commit(b_kempty((it + 1) % C::KS));
+                if (j + 2 == nb) mma_commit(b_qempty);
+              }
+            } else {
+              mma_commit(b_ofull(i));
+            }
+          }
+          if (!ok) break;
+          mma_commit(b_vempty(vs));
+        }
+        if (!ok) break;
+      }
+      // every issued MMA completes before teardown frees TMEM
+      mma_commit(b_done);
+      const uint64_t t0 = globaltimer_ns();
+      drain_wait(b_done, 0, t0, tmo);
+    }
+  } else if (warp >= 4) {
+    // ================= softmax of tile i, one row per thread ==========================
+    const int i = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t t_o = t_row + C::COL_O + i * D;
+    const int row_tok = row / G, row_g = row - row_tok * G;
+    int cnt = 0, it = 0, nseg = 0;  // blocks of this tile / of the CTA, segments of this tile
+    bool ok = true;
+    for (; ok && walk.next(prm.tiles, prm.cum); it += walk.nb, walk.advance()) {
+      const int ntok = walk.tile.ntok - i * TOK;
+      if (ntok <= 0) continue;  // a lone tile: the second group of warps has no rows
+      const int token = walk.tile.tok0 + i * TOK + row_tok;
+      const int pos = walk.tile.pos0 + i * TOK + row_tok;
+      const bool row_valid = row_tok < min(TOK, ntok);
+      const int head = walk.hk * G + row_g;
+      int lo = 0, hi = -1;
+      float slope = 0.f;
+      if (row_valid) {
+        token_range(prm.mask, token, pos, walk.tile.kv, walk.tile.prefix, lo, hi);
+        if (BIAS) slope = __ldg(prm.slopes + head) * 1.4426950408889634f;
+      }
+      const bool warp_works = __any_sync(0xffffffffu, row_valid);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < walk.nb; ++j, ++cnt) {
+        const int sbuf = NT == 1 ? cnt & 1 : i;
+        const uint32_t t_s = t_row + sbuf * 128;
+        if (!wait_warp_hot(b_sfull(sbuf), (NT == 1 ? cnt >> 1 : cnt) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const int key0 = (walk.jb + j) * C::KB;
+        // rows without a token never need the mask: their result goes nowhere
+        const bool inside = !row_valid || (lo <= key0 && hi >= key0 + C::KB - 1);
+        if (warp_works) {
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+          auto block = [&](auto mask_tag) {
+            constexpr bool MASK = decltype(mask_tag)::value;
+            const int rlo = lo - key0, rhi = hi - key0;
+            const float dist0 = (float)(key0 - pos);
+            auto seen = [&](int e) { return !MASK || (e >= rlo && e <= rhi); };
+            // score in log2 units
+            auto val = [&](uint32_t v, int e) {
+              float x = score_log2<CAP>(prm.score, __uint_as_float(v));
+              if (BIAS) x = fmaf(-slope, fabsf(dist0 + (float)e), x);
+              return seen(e) ? x : -INFINITY;
+            };
+            // for the row max, without a bias: the raw product (the cap is monotone)
+            auto raw = [&](uint32_t v, int e) {
+              if (BIAS) return val(v, e);
+              return seen(e) ? __uint_as_float(v) : -INFINITY;
+            };
+            float m_loc;
+            {
+              uint32_t sa[64], sb[64];
+              tmem_ld64_async(t_s, sa);
+              tmem_ld64_async(t_s + 64, sb);
+              tmem_ld_wait64x2(sa, sb);
+              float a[8];
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                a[e & 7] = e < 8 ? raw(sa[e], e) : fmaxf(a[e & 7], raw(sa[e], e));
+#pragma unroll
+              for (int e = 0; e < 64; ++e) a[e & 7] = fmaxf(a[e & 7], raw(sb[e], 64 + e));
+#pragma unroll
+              for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+                for (int e = 0; e < w; ++e) a[e] = fmaxf(a[e], a[e + w]);
+              m_loc = a[0];
+              if (!BIAS && m_loc != -INFINITY) m_loc = score_log2<CAP>(prm.score, m_loc);
+            }
+            const bool resc = m_loc > m_ref + C::kRescale;
+            if (j > 0 && __any_sync(0xffffffffu, resc)) {
+              if (NT == 1) {  // O is at rest once the previous block's product is done
+                if (!wait_warp(b_pv, (cnt - 1) & 1)) return false;
+                tc_fence_after();
+              }
+              const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
+#pragma unroll 1
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t r[32];
+                tmem_ld32(t_o + k * 32, r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st32(t_o + k * 32, r);
+              }
+              tmem_st_wait();
+              l *= alpha;
+            }
+            if (resc) m_ref = m_loc;
+            const float nb2 = m_ref == -INFINITY ? 0.f : -m_ref;
+            uint32_t va[32], vb[32], w[16];
+            tmem_ld32_async(t_s, va);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t* cur = (c & 1) ? vb : va;
+              uint32_t* nxt = (c & 1) ? va : vb;
+              tmem_ld_wait32(cur);
+              if (c < 3) tmem_ld32_async(t_s + (c + 1) * 32, nxt);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int x = c * 32 + 2 * e;
+                float x0, x1;
+                if (!CAP && !BIAS) {
+                  x0 = seen(x) ? fmaf(__uint_as_float(cur[2 * e]), prm.score.a, nb2) : -INFINITY;
+                  x1 = seen(x + 1) ? fmaf(__uint_as_float(cur[2 * e + 1]), prm.score.a, nb2)
+                                   : -INFINITY;
+                } else {
+                  x0 = val(cur[2 * e], x) + nb2;
+                  x1 = val(cur[2 * e + 1], x + 1) + nb2;
+                }
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                rs[e & 3] += p0;
+                rs[(e + 2) & 3] += p1;
+                __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+                w[e] = *reinterpret_cast<uint32_t*>(&v2);
+              }
+              tmem_st16(t_s + c * 16, w);
+            }
+            return true;
+          };
+          ok = __all_sync(0xffffffffu, inside) ? block(std::false_type{}) : block(std::true_type{});
+          l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        // one barrier a buffer: with one tile a warp without rows may be a block ahead of the
+        // others, and its arrival must not count for theirs
+        if (lane == 0) mbar_arrive(b_pfull(sbuf));
+        if (!ok) break;
+      }
+      // ---- epilogue: O / l, or the partial rows of a tile cut between CTAs
+      const bool have = ok && wait_warp(b_ofull(i), nseg & 1);
+      ++nseg;
+      if (!have) ok = false;
+      if (!have || !warp_works) continue;
+      tc_fence_after();
+      const bool whole = walk.part < 0;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long r_out = (long long)token * prm.num_q_heads + head;
+      const long long r_part =
+          (long long)(2 * blockIdx.x + (walk.part > 0 ? 1 : 0)) * prm.part_rows + i * 128 + row;
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t r[32];
+        tmem_ld32(t_o + k * 32, r);
+        if (!row_valid) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(r[2 * e]) * inv,
+                                                      __uint_as_float(r[2 * e + 1]) * inv);
+            w[e] = *reinterpret_cast<uint32_t*>(&v2);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(prm.out + r_out * D + k * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(prm.part_o + r_part * D + k * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+        }
+      }
+      if (row_valid) {
+        if (whole) {
+          if (prm.lse)
+            prm.lse[r_out] = l > 0.f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          prm.part_ml[r_part] = make_float2(m_ref, l);
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp == 3) {
+    // ================= the join list ==================================================
+    ChunkJoin jn;
+    jn.ntok = jn.tok0 = jn.hk = jn.last = 0;
+    while (walk.next(prm.tiles, prm.cum)) {
+      if (walk.part == 1) {
+        jn.tok0 = walk.tile.tok0;
+        jn.ntok = walk.tile.ntok;
+        jn.hk = walk.hk;
+        jn.last = (int)((walk.w + walk.tile.nb - 1) / quota);
+      }
+      walk.advance();
+    }
+    if (lane == 0) {
+      ChunkJoin* o = prm.joins + blockIdx.x;
+      o->tok0 = jn.tok0;
+      o->ntok = jn.ntok;
+      o->hk = jn.hk;
+      o->last = jn.last;
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- join of the tiles that were cut ----------------------------------------------------
+constexpr int JOIN_WARPS = 8;
+
+// grid (NUM_SMS, row groups); one row a warp
+template <int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const ChunkAttnParams p) {
+  constexpr int EPL = D / 32;  // floats a lane
+  pdl_wait();
+  const int4 jn = __ldcg(reinterpret_cast<const int4*>(p.joins + blockIdx.x));
+  if (!jn.x) return;  // ntok = 0: this CTA cut no tile
+  const int last = __ldcg(&p.joins[blockIdx.x].last);
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
+  const int G = p.group, r = row & 127;
+  const int tok = (row >> 7) * p.tile_tokens + r / G;
+  if (r >= p.tile_tokens * G || tok >= jn.x) return;
+  const int c0 = blockIdx.x, n = last - c0 + 1;
+  auto slot = [&](int s) { return (long long)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.part_rows + row; };
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldcg(p.part_ml + slot(s)).x);
+  m = warp_max(m);
+  float l = 0.f, o[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+  if (m != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const long long at = slot(s);
+      const float2 ml = __ldcg(p.part_ml + at);
+      const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - m) : 0.f;
+      l = fmaf(w, ml.y, l);
+      const float* src = p.part_o + at * D + lane * EPL;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, __ldcg(src + e), o[e]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const long long out = (long long)(jn.y + tok) * p.num_q_heads + jn.z * G + r % G;
+#pragma unroll
+  for (int e = 0; e < EPL; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(p.out + out * D + lane * EPL + e) =
+        __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace cosa

@@ -16,6 +16,10 @@
 #include "attn_dense.cuh"
 #include "attn_gqa.cuh"
 #include "decode.cuh"
+#include "chunk_write.cuh"
+#include "chunk_attn.cuh"
+#include "attn_mass.cuh"
+#include "evict.cuh"
 
 using namespace cosa;
 
@@ -409,6 +413,199 @@ cosa_status_t launch_decode_t(const DecodeParams& prm, int bh, cudaStream_t st) 
   if (last_launch() != COSA_OK) return COSA_ERR_CUDA;
   decode_pv_kernel<D, P><<<grid, DEC_THREADS, 0, st>>>(prm);
   return last_launch();
+}
+
+// ---- a chunk of new tokens over the paged cache -----------------------------------------
+cosa_status_t check_chunk(const cosa_chunk_t* s) {
+  if (!s) return COSA_ERR_INVALID_ARG;
+  if (s->batch <= 0 || s->num_q_heads <= 0 || s->num_kv_heads <= 0 || s->head_dim <= 0 ||
+      s->page_size <= 0 || s->total_q <= 0 || s->max_q <= 0 || s->max_kv <= 0 ||
+      s->pages_per_seq <= 0 || s->num_phys_pages <= 0)
+    return COSA_ERR_INVALID_ARG;
+  if (!(s->softmax_scale > 0.f) || !std::isfinite(s->softmax_scale)) return COSA_ERR_INVALID_ARG;
+  if (s->num_q_heads % s->num_kv_heads) return COSA_ERR_INVALID_ARG;
+  if (s->max_q > s->total_q || s->max_q > s->max_kv ||
+      s->max_kv > (long long)s->pages_per_seq * s->page_size)
+    return COSA_ERR_INVALID_ARG;
+  if (s->head_dim != 64 && s->head_dim != 128) return COSA_ERR_UNSUPPORTED;
+  if (s->page_size != 16 && s->page_size != 32 && s->page_size != 64 && s->page_size != 128)
+    return COSA_ERR_UNSUPPORTED;
+  if (s->num_q_heads / s->num_kv_heads > 128 || s->batch > CHUNK_MAX_BATCH ||
+      s->num_kv_heads > 65535)
+    return COSA_ERR_UNSUPPORTED;
+  // token and key counts stay in 32 bits, offsets in 64; TMA coordinates are 32-bit
+  if (s->max_kv > (1 << 30) || s->total_q > (1 << 30) ||
+      (long long)s->pages_per_seq * s->page_size > (1ll << 30) ||
+      (long long)s->num_phys_pages * s->num_kv_heads > 0x7fffffffll)
+    return COSA_ERR_UNSUPPORTED;
+  return COSA_OK;
+}
+
+cosa_status_t check_score(const cosa_score_params_t* s) {
+  if (!s) return COSA_OK;
+  if (!(s->softcap >= 0.f) || !std::isfinite(s->softcap) || s->window < 0)
+    return COSA_ERR_INVALID_ARG;
+  return COSA_OK;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// row stride of a token-major tensor of H heads
+bool good_stride(int64_t stride, int heads, int D) {
+  return stride >= (int64_t)heads * D && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+ChunkSeqs chunk_seqs(const cosa_chunk_t* s, const int32_t* cu_q, const int32_t* kv_len) {
+  return ChunkSeqs{cu_q, kv_len, s->batch, s->total_q, s->max_q, s->max_kv};
+}
+
+ChunkMask chunk_mask(const cosa_score_params_t* s) {
+  if (!s) return ChunkMask{nullptr, nullptr, 0};
+  return ChunkMask{s->first_key, s->prefix_len, s->window};
+}
+
+ScoreShape score_shape(const cosa_chunk_t* s, const cosa_score_params_t* sc) {
+  const float log2e = 1.4426950408889634f;
+  if (sc && sc->softcap > 0.f)
+    return ScoreShape{(float)(2.0 * s->softmax_scale / sc->softcap * 1.4426950408889634),
+                      sc->softcap * log2e};
+  return ScoreShape{s->softmax_scale * log2e, 0.f};
+}
+
+// bf16 [tokens][heads][D] with a token stride: box = 64 columns x G heads x `tokens` tokens
+bool make_map_q(CUtensorMap* m, const void* base, const cosa_chunk_t* s, int64_t stride) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int G = s->num_q_heads / s->num_kv_heads;
+  cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_q_heads,
+                        (cuuint64_t)s->total_q};
+  cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of cosa_chunk_attention: the plan (tiles, their running block count, their
+// number), the join list and the partial rows of tiles cut between CTAs.
+struct ChunkLayout {
+  size_t tiles, cum, n_tiles, joins, part_ml, part_o, total;
+  int nt, part_rows, max_tiles;
+};
+
+ChunkLayout chunk_layout(const cosa_chunk_t* s) {
+  ChunkLayout L;
+  const int G = s->num_q_heads / s->num_kv_heads, tok = 128 / G;
+  // one tile at a time while a sequence's rows fit in it: a pair would leave its second
+  // softmax group idle (one tile with two S buffers keeps the cache stream running)
+  L.nt = s->max_q <= tok ? 1 : 2;
+  L.part_rows = L.nt == 2 ? 256 : s->max_q * G;
+  const size_t span = (size_t)tok * L.nt;
+  const size_t by_tokens = s->total_q / span + s->batch;
+  const size_t by_seqs = (size_t)s->batch * ((s->max_q + span - 1) / span);
+  const size_t T = by_tokens < by_seqs ? by_tokens : by_seqs;
+  const size_t slots = 2 * NUM_SMS;
+  L.max_tiles = (int)T;
+  size_t off = 0;
+  L.tiles = off;
+  off = align256(off + T * sizeof(ChunkTile));
+  L.cum = off;
+  off = align256(off + (T + 1) * sizeof(long long));
+  L.n_tiles = off;
+  off = align256(off + sizeof(int));
+  L.joins = off;
+  off = align256(off + NUM_SMS * sizeof(ChunkJoin));
+  L.part_ml = off;
+  off = align256(off + slots * L.part_rows * sizeof(float2));
+  L.part_o = off;
+  off = align256(off + slots * L.part_rows * s->head_dim * sizeof(float));
+  L.total = off;
+  return L;
+}
+
+// a launch whose prologue may overlap the end of the kernel before it
+template <typename... KArgs, typename... Args>
+cosa_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return COSA_ERR_CUDA;
+  }
+  return COSA_OK;
+}
+
+template <int D, int NT, bool CAP, bool BIAS>
+cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, const void* q,
+                             int64_t q_stride, const void* k_pool, const void* v_pool,
+                             cudaStream_t st) {
+  using Cfg = ChunkCfg<D, NT>;
+  CUtensorMap mq, mk, mv;
+  const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
+  if (!make_map_q(&mq, q, s, q_stride) || !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size) ||
+      !make_map(&mv, v_pool, D, s->page_size, PZ, s->page_size))
+    return COSA_ERR_CUDA;
+  auto kern = chunk_attn_kernel<D, NT, CAP, BIAS>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Cfg::SMEM_ALLOC) != cudaSuccess)
+    return COSA_ERR_CUDA;
+  chunk_plan_kernel<<<1, PLAN_THREADS, (size_t)(s->batch + 1) * sizeof(int), st>>>(prm);
+  cosa_status_t e = last_launch();
+  if (e != COSA_OK) return e;
+  e = launch_pdl(kern, dim3(NUM_SMS), Cfg::THREADS, Cfg::SMEM_ALLOC, st, mq, mk, mv, prm);
+  if (e != COSA_OK) return e;
+  return launch_pdl(chunk_combine_kernel<D>,
+                    dim3(NUM_SMS, (prm.part_rows + JOIN_WARPS - 1) / JOIN_WARPS), 32 * JOIN_WARPS,
+                    0, st, prm);
+}
+
+template <int D, int NT>
+cosa_status_t launch_chunk_n(const cosa_chunk_t* s, const ChunkAttnParams& prm, bool cap,
+                             const void* q, int64_t q_stride, const void* k_pool,
+                             const void* v_pool, cudaStream_t st) {
+  const bool bias = prm.slopes != nullptr;
+  if (cap && bias) return launch_chunk_t<D, NT, true, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (cap) return launch_chunk_t<D, NT, true, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (bias) return launch_chunk_t<D, NT, false, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  return launch_chunk_t<D, NT, false, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+}
+
+template <int D, bool CAP, bool BIAS>
+cosa_status_t launch_mass_t(const cosa_chunk_t* s, const MassParams& prm, const void* q,
+                            int64_t q_stride, const void* k_pool, dim3 grid, cudaStream_t st) {
+  using Cfg = MassCfg<D>;
+  CUtensorMap mq, mk;
+  const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
+  if (!make_map_q(&mq, q, s, q_stride) || !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size))
+    return COSA_ERR_CUDA;
+  auto kern = attn_mass_kernel<D, CAP, BIAS>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Cfg::SMEM_ALLOC) != cudaSuccess)
+    return COSA_ERR_CUDA;
+  kern<<<grid, Cfg::THREADS, Cfg::SMEM_ALLOC, st>>>(mq, mk, prm);
+  return last_launch();
+}
+
+template <int D>
+cosa_status_t launch_mass_d(const cosa_chunk_t* s, const MassParams& prm, bool cap, const void* q,
+                            int64_t q_stride, const void* k_pool, dim3 grid, cudaStream_t st) {
+  const bool bias = prm.slopes != nullptr;
+  if (cap && bias) return launch_mass_t<D, true, true>(s, prm, q, q_stride, k_pool, grid, st);
+  if (cap) return launch_mass_t<D, true, false>(s, prm, q, q_stride, k_pool, grid, st);
+  if (bias) return launch_mass_t<D, false, true>(s, prm, q, q_stride, k_pool, grid, st);
+  return launch_mass_t<D, false, false>(s, prm, q, q_stride, k_pool, grid, st);
 }
 
 // Test hook of cosa_debug_osk_wait_fault: one-shot, per host thread.
@@ -970,6 +1167,243 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
   t_osk_fault.k_group = withhold_k_group;
   t_osk_fault.wait_limit_ns = wait_limit_ns;
   return COSA_OK;
+}
+
+cosa_status_t cosa_chunk_write(const cosa_chunk_t* shape, const cosa_rope_params_t* rope,
+                               const void* q_tok, int64_t q_tok_stride, const void* k_tok,
+                               int64_t k_tok_stride, const void* v_tok, int64_t v_tok_stride,
+                               const int32_t* positions, const float* inv_freq,
+                               const int32_t* cu_q, const int32_t* kv_len,
+                               const int32_t* page_table, void* q, int64_t q_stride,
+                               void* k_pool, void* v_pool, cosa_stream_t stream) {
+  cosa_status_t e = check_chunk(shape);
+  if (e != COSA_OK) return e;
+  const int D = shape->head_dim, Hq = shape->num_q_heads, Hk = shape->num_kv_heads;
+  ChunkWriteParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (rope && rope->axes != 0) {
+    if (rope->axes < 0 || rope->axes > COSA_MAX_ROPE_AXES) return COSA_ERR_INVALID_ARG;
+    if ((rope->interleaved != 0 && rope->interleaved != 1) ||
+        (rope->adjacent != 0 && rope->adjacent != 1))
+      return COSA_ERR_INVALID_ARG;
+    long long half = 0;
+    for (int a = 0; a < rope->axes; ++a) {
+      if (rope->sections[a] < 0) return COSA_ERR_INVALID_ARG;
+      half += rope->sections[a];
+      p.sections[a] = rope->sections[a];
+    }
+    if (half == 0 || 2 * half > D) return COSA_ERR_INVALID_ARG;
+    if (half % 8) return COSA_ERR_UNSUPPORTED;
+    if (!positions || !inv_freq) return COSA_ERR_INVALID_ARG;
+    p.half = (int)half;
+    p.axes = rope->axes;
+    p.interleaved = rope->interleaved;
+    p.adjacent = rope->adjacent;
+  }
+  if (!q_tok || !k_tok || !v_tok || !cu_q || !kv_len || !page_table || !q || !k_pool || !v_pool)
+    return COSA_ERR_INVALID_ARG;
+  if (!aligned16(q_tok) || !aligned16(k_tok) || !aligned16(v_tok) || !aligned16(q) ||
+      !aligned16(k_pool) || !aligned16(v_pool))
+    return COSA_ERR_INVALID_ARG;
+  if (!good_stride(q_tok_stride, Hq, D) || !good_stride(k_tok_stride, Hk, D) ||
+      !good_stride(v_tok_stride, Hk, D) || !good_stride(q_stride, Hq, D))
+    return COSA_ERR_INVALID_ARG;
+  if (q == q_tok && q_stride != q_tok_stride) return COSA_ERR_INVALID_ARG;
+  p.seqs = chunk_seqs(shape, cu_q, kv_len);
+  p.q_tok = reinterpret_cast<const __nv_bfloat16*>(q_tok);
+  p.k_tok = reinterpret_cast<const __nv_bfloat16*>(k_tok);
+  p.v_tok = reinterpret_cast<const __nv_bfloat16*>(v_tok);
+  p.q = reinterpret_cast<__nv_bfloat16*>(q);
+  p.k_pool = reinterpret_cast<__nv_bfloat16*>(k_pool);
+  p.v_pool = reinterpret_cast<__nv_bfloat16*>(v_pool);
+  p.q_tok_stride = q_tok_stride;
+  p.k_tok_stride = k_tok_stride;
+  p.v_tok_stride = v_tok_stride;
+  p.q_stride = q_stride;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.page_table = page_table;
+  p.num_q_heads = Hq;
+  p.num_kv_heads = Hk;
+  p.page_size = shape->page_size;
+  p.pages_per_seq = shape->pages_per_seq;
+  p.num_phys_pages = shape->num_phys_pages;
+  const long long units = (long long)(Hq + 2 * Hk) * (D / 16);
+  if (units > (1 << 26)) return COSA_ERR_UNSUPPORTED;
+  // tokens share a CTA's setup while four CTAs an SM are left; a few tokens are split by
+  // heads instead, one unit a thread
+  long long tpb = shape->total_q / (4 * NUM_SMS);
+  p.tokens_per_cta = tpb < 1 ? 1 : (tpb > 8 ? 8 : (int)tpb);
+  const int blocks = (shape->total_q + p.tokens_per_cta - 1) / p.tokens_per_cta;
+  p.units_per_part = (int)units;
+  if (blocks < 2 * NUM_SMS && units > CHUNK_WRITE_THREADS)
+    p.units_per_part = CHUNK_WRITE_THREADS;
+  const long long parts = (units + p.units_per_part - 1) / p.units_per_part;
+  if (parts > 65535) return COSA_ERR_UNSUPPORTED;
+  const size_t smem = (size_t)p.tokens_per_cta * p.half * 8;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  dim3 grid(blocks, (unsigned)parts);
+  if (D == 128) chunk_write_kernel<128><<<grid, CHUNK_WRITE_THREADS, smem, st>>>(p);
+  else chunk_write_kernel<64><<<grid, CHUNK_WRITE_THREADS, smem, st>>>(p);
+  return last_launch();
+}
+
+cosa_status_t cosa_chunk_attention_workspace_size(const cosa_chunk_t* shape, size_t* bytes) {
+  cosa_status_t e = check_chunk(shape);
+  if (e != COSA_OK) return e;
+  if (!bytes) return COSA_ERR_INVALID_ARG;
+  *bytes = chunk_layout(shape).total;
+  return COSA_OK;
+}
+
+cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_params_t* score,
+                                   const void* q, int64_t q_stride, const void* k_pool,
+                                   const void* v_pool, const int32_t* page_table,
+                                   const int32_t* cu_q, const int32_t* kv_len, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   cosa_stream_t stream) {
+  cosa_status_t e = check_chunk(shape);
+  if (e == COSA_OK) e = check_score(score);
+  if (e != COSA_OK) return e;
+  if (!q || !k_pool || !v_pool || !page_table || !cu_q || !kv_len || !out)
+    return COSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return COSA_ERR_INVALID_ARG;
+  if (!good_stride(q_stride, shape->num_q_heads, shape->head_dim)) return COSA_ERR_INVALID_ARG;
+  const ChunkLayout L = chunk_layout(shape);
+  if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return COSA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ChunkAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.seqs = chunk_seqs(shape, cu_q, kv_len);
+  p.mask = chunk_mask(score);
+  p.page_table = page_table;
+  p.slopes = score ? score->slopes : nullptr;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.tiles = reinterpret_cast<ChunkTile*>(ws + L.tiles);
+  p.cum = reinterpret_cast<long long*>(ws + L.cum);
+  p.n_tiles = reinterpret_cast<int*>(ws + L.n_tiles);
+  p.joins = reinterpret_cast<ChunkJoin*>(ws + L.joins);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.num_q_heads = shape->num_q_heads;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.group = shape->num_q_heads / shape->num_kv_heads;
+  p.page_size = shape->page_size;
+  p.pages_per_seq = shape->pages_per_seq;
+  p.num_phys_pages = shape->num_phys_pages;
+  p.tile_tokens = 128 / p.group;
+  p.nt = L.nt;
+  p.part_rows = L.part_rows;
+  p.max_tiles = L.max_tiles;
+  p.score = score_shape(shape, score);
+  p.timeout_ns = kWaitTimeoutNs;
+  const bool cap = score && score->softcap > 0.f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (shape->head_dim == 128)
+    return L.nt == 1 ? launch_chunk_n<128, 1>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
+                     : launch_chunk_n<128, 2>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
+  return L.nt == 1 ? launch_chunk_n<64, 1>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
+                   : launch_chunk_n<64, 2>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
+}
+
+cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_params_t* score,
+                                  const void* q, int64_t q_stride, const void* k_pool,
+                                  const int32_t* page_table, const int32_t* cu_q,
+                                  const int32_t* kv_len, const float* lse, int32_t last_q,
+                                  float decay, float* mass, cosa_stream_t stream) {
+  cosa_status_t e = check_chunk(shape);
+  if (e == COSA_OK) e = check_score(score);
+  if (e != COSA_OK) return e;
+  if (!q || !k_pool || !page_table || !cu_q || !kv_len || !lse || !mass)
+    return COSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || last_q < 0 || !(decay >= 0.f) ||
+      !std::isfinite(decay))
+    return COSA_ERR_INVALID_ARG;
+  if (!good_stride(q_stride, shape->num_q_heads, shape->head_dim)) return COSA_ERR_INVALID_ARG;
+  if (shape->batch > 65535) return COSA_ERR_UNSUPPORTED;
+  MassParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.seqs = chunk_seqs(shape, cu_q, kv_len);
+  p.mask = chunk_mask(score);
+  p.page_table = page_table;
+  p.slopes = score ? score->slopes : nullptr;
+  p.lse = lse;
+  p.mass = mass;
+  p.mass_stride = (long long)shape->pages_per_seq * shape->page_size;
+  p.num_q_heads = shape->num_q_heads;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.group = shape->num_q_heads / shape->num_kv_heads;
+  p.page_size = shape->page_size;
+  p.pages_per_seq = shape->pages_per_seq;
+  p.num_phys_pages = shape->num_phys_pages;
+  p.tile_tokens = 128 / p.group;
+  p.last_q = last_q;
+  int rows = last_q > 0 && last_q < shape->max_q ? last_q : shape->max_q;
+  rows = (rows < p.tile_tokens ? rows : p.tile_tokens) * p.group;
+  p.cols = (rows + 15) / 16 * 16;
+  p.decay = decay;
+  p.score = score_shape(shape, score);
+  p.timeout_ns = kWaitTimeoutNs;
+  // runs of key blocks: enough for several CTAs an SM over the whole call
+  const long long bh = (long long)shape->batch * shape->num_kv_heads;
+  const long long nblk = ((long long)shape->max_kv + 127) / 128;
+  long long parts = (4 * NUM_SMS + bh - 1) / bh;
+  if (parts > nblk) parts = nblk;
+  dim3 grid((unsigned)parts, shape->num_kv_heads, shape->batch);
+  const bool cap = score && score->softcap > 0.f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return shape->head_dim == 128 ? launch_mass_d<128>(shape, p, cap, q, q_stride, k_pool, grid, st)
+                                : launch_mass_d<64>(shape, p, cap, q, q_stride, k_pool, grid, st);
+}
+
+cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_params_t* evict,
+                               void* k_pool, void* v_pool, const int32_t* page_table,
+                               const int32_t* kv_len, const float* mass,
+                               const int32_t* dst_table, int32_t* kept, int32_t* new_len,
+                               float* mass_out, cosa_stream_t stream) {
+  cosa_status_t e = check_chunk(shape);
+  if (e != COSA_OK) return e;
+  if (!evict || evict->budget <= 0 || evict->sink < 0 || evict->recent < 0 ||
+      (long long)evict->sink + evict->recent > evict->budget)
+    return COSA_ERR_INVALID_ARG;
+  if (!k_pool || !v_pool || !page_table || !kv_len || !mass || !dst_table || !kept || !new_len)
+    return COSA_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return COSA_ERR_INVALID_ARG;
+  if (evict->budget > (1 << 30)) return COSA_ERR_UNSUPPORTED;
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.mass = mass;
+  p.kv_len = kv_len;
+  p.page_table = page_table;
+  p.dst_table = dst_table;
+  p.k_pool = reinterpret_cast<__nv_bfloat16*>(k_pool);
+  p.v_pool = reinterpret_cast<__nv_bfloat16*>(v_pool);
+  p.kept = kept;
+  p.new_len = new_len;
+  p.mass_out = mass_out;
+  p.mass_stride = (long long)shape->pages_per_seq * shape->page_size;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.page_size = shape->page_size;
+  p.pages_per_seq = shape->pages_per_seq;
+  p.num_phys_pages = shape->num_phys_pages;
+  p.max_kv = shape->max_kv;
+  p.dst_pages = (evict->budget + shape->page_size - 1) / shape->page_size;
+  p.budget = evict->budget;
+  p.sink = evict->sink;
+  p.recent = evict->recent;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  evict_select_kernel<<<dim3(EVICT_CL, shape->num_kv_heads, shape->batch), EVICT_THREADS, 0, st>>>(p);
+  e = last_launch();
+  if (e != COSA_OK) return e;
+  const int most = evict->budget < shape->max_kv ? evict->budget : shape->max_kv;
+  const int rows = GATHER_THREADS / (shape->head_dim / 8) * GATHER_UNROLL;
+  dim3 grid((most + rows - 1) / rows, shape->num_kv_heads, shape->batch);
+  if (shape->head_dim == 128) evict_gather_kernel<128><<<grid, GATHER_THREADS, 0, st>>>(p);
+  else evict_gather_kernel<64><<<grid, GATHER_THREADS, 0, st>>>(p);
+  return last_launch();
 }
 
 cosa_status_t cosa_get_status(cosa_stream_t stream) {

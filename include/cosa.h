@@ -385,6 +385,148 @@ cosa_status_t cosa_attention_host(const cosa_shape_t* shape, const cosa_kap_para
  * Host-only; no CUDA call. */
 cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_limit_ns);
 
+/* ---- A chunk of new tokens over the paged cache ---------------------------------------
+ * The calls above take whole prompts: queries 0..N-1, N a multiple of the page.  The
+ * four calls below serve the cache between prompts, for ragged batches: each sequence
+ * brings a chunk of new tokens (a piece of a prompt, an image, one decoded token) that
+ * is rotated and written behind its keys (cosa_chunk_write), attends to the whole cache
+ * (cosa_chunk_attention), adds its attention to each key's mass (cosa_attention_mass),
+ * and the cache is cut to the heaviest keys (cosa_cache_evict).  The pages describe
+ * prefill only (gist.science/pt §2.3 takes queries and keys of one whole prompt); this is
+ * plain exact attention over the same cache layout, beside the sparse path.
+ *
+ * Layouts: the new tokens of all sequences are rows of token-major tensors,
+ *   [total_q][H][D] bf16, sequence b owning rows cu_q[b] .. cu_q[b+1]-1
+ *   (cu_q int32 [B+1], device).  kv_len int32 [B] (device) is sequence b's number of keys
+ *   INCLUDING its new tokens: new token i (of q_len = cu_q[b+1] - cu_q[b]) sits at cache
+ *   position t = kv_len - q_len + i.  Pools and page table are those above, with
+ *   P in {16, 32, 64, 128}.  Rows at and past cu_q[B] are neither read into a result nor
+ *   written.  A sequence without new tokens is left alone.
+ * Row strides (in elements) let q_tok / k_tok / v_tok / q be views of a fused
+ * projection's output: at least H * D, a multiple of 8, heads contiguous.
+ * Lengths are checked on the device: a sequence with cu_q decreasing or past total_q,
+ * q_len > max_q, kv_len > max_kv or q_len > kv_len is recorded as COSA_ERR_INVALID_ARG in
+ * the status word and left out (its outputs keep what they held).  A page-table entry
+ * outside the pool is recorded the same way; its keys read as zeros and nothing is
+ * written there.  Keys are addressed by cache position: after an eviction, positions
+ * (and the window and distances below) count the kept keys, while the rotation of
+ * cosa_chunk_write takes its own position values. */
+typedef struct {
+  int32_t batch;          /* B, at most 8192                                       */
+  int32_t num_q_heads;    /* H_q                                                   */
+  int32_t num_kv_heads;   /* H_kv, divides H_q; H_q / H_kv <= 128                  */
+  int32_t head_dim;       /* D, 64 or 128                                          */
+  int32_t page_size;      /* P, 16, 32, 64 or 128                                  */
+  int32_t total_q;        /* rows of the token-major tensors, >= cu_q[B]           */
+  int32_t max_q;          /* bound on a sequence's new tokens, <= total_q          */
+  int32_t max_kv;         /* bound on kv_len, <= pages_per_seq * P                 */
+  int32_t pages_per_seq;  /* row stride of page_table                              */
+  int32_t num_phys_pages; /* rows of k_pool / v_pool                               */
+  float softmax_scale;    /* multiplies q.k (usually 1/sqrt(D))                    */
+} cosa_chunk_t;
+
+#define COSA_MAX_ROPE_AXES 4
+
+/* Rotary positions with one or several axes (time, height, width, ...).  The first
+ * 2 * sum(sections) dims of each Q and K head are rotated in pairs, pair j by the angle
+ * positions[axis(j)][token] * inv_freq[j]; the other dims and V are copied. */
+typedef struct {
+  int32_t axes;                         /* 1 .. COSA_MAX_ROPE_AXES; 0: no rotation       */
+  int32_t sections[COSA_MAX_ROPE_AXES]; /* pairs of each axis, >= 0; the rotated dims
+                                           (twice their sum) a multiple of 16, <= D      */
+  int32_t interleaved;                  /* 0: the pairs of axis 0 first, then axis 1, ...
+                                           1: pair j belongs to axis a = j mod axes if
+                                           a > 0 and j < axes * sections[a], else axis 0 */
+  int32_t adjacent;                     /* 0: pair j is dims (j, j + rotated / 2);
+                                           1: pair j is dims (2j, 2j + 1)                */
+} cosa_rope_params_t;
+
+/* How scores are shaped and which keys a token sees.  NULL means plain causal. */
+typedef struct {
+  float softcap;             /* c > 0: s <- c * tanh(s / c) on the scaled score; 0: off  */
+  int32_t window;            /* w > 0: keys older than t - w + 1 are not seen; 0: off    */
+  const float* slopes;       /* fp32 [H_q] or NULL: s <- s - slopes[h] * |t - key| (after
+                                the cap): a bias that depends on distance                */
+  const int32_t* first_key;  /* int32 [total_q] or NULL: the first key each token sees,
+                                its document's first token in a packed sequence; past
+                                the token's last key: the token sees nothing             */
+  const int32_t* prefix_len; /* int32 [B] or NULL: keys below prefix_len[b] are seen by
+                                every token of the sequence, later ones too              */
+} cosa_score_params_t;
+/* A token at position t sees key k iff k < kv_len, k >= max(first_key, t - window + 1),
+ * and k <= t or k < prefix_len.  A token that sees no key gets a zero output row and lse
+ * -inf.  Keys and values at and past kv_len may hold anything (NaN included); V of the keys
+ * below kv_len must be finite, since a value that one row of a tile does not see is
+ * multiplied by a zero weight. */
+
+/* Rotate and append: writes q[token] = rotate(q_tok[token]) and, at each token's cache
+ * position, K = rotate(k_tok) and V = v_tok.  positions int32 [axes][total_q] and
+ * inv_freq fp32 [sum(sections)] are device arrays (both unused when rope is NULL or
+ * rope->axes is 0: a plain append).  Angles are taken in 64 bits (far positions keep
+ * their phase), the rotation in fp32 and rounded once.  q may be q_tok (same stride):
+ * rotation in place.  No page may hold new tokens of two sequences. */
+cosa_status_t cosa_chunk_write(const cosa_chunk_t* shape, const cosa_rope_params_t* rope,
+                               const void* q_tok, int64_t q_tok_stride, const void* k_tok,
+                               int64_t k_tok_stride, const void* v_tok, int64_t v_tok_stride,
+                               const int32_t* positions, const float* inv_freq,
+                               const int32_t* cu_q, const int32_t* kv_len,
+                               const int32_t* page_table, void* q, int64_t q_stride,
+                               void* k_pool, void* v_pool, cosa_stream_t stream);
+
+/* Bytes of device workspace cosa_chunk_attention needs.  Host-only; no CUDA call. */
+cosa_status_t cosa_chunk_attention_workspace_size(const cosa_chunk_t* shape, size_t* bytes);
+
+/* Exact attention of every sequence's new tokens over its cache (the new tokens' own keys
+ * included: queue it after cosa_chunk_write).  q bf16 [total_q][H_q][D] with row stride
+ * q_stride; out bf16 [total_q][H_q][D] and lse fp32 [total_q][H_q] (natural log, may be
+ * NULL), dense.  From one new token a sequence (decode) to whole prompts.  workspace:
+ * at least cosa_chunk_attention_workspace_size bytes, 256-byte aligned, contents on entry
+ * do not matter; calls that may overlap on the GPU need one each. */
+cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_params_t* score,
+                                   const void* q, int64_t q_stride, const void* k_pool,
+                                   const void* v_pool, const int32_t* page_table,
+                                   const int32_t* cu_q, const int32_t* kv_len, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   cosa_stream_t stream);
+
+/* Attention mass of the cached keys: with w = exp(s - lse) the attention weights of the
+ * call whose lse is given (same q, score and lengths),
+ *   mass[b][h_kv][k] = (k < kv_len - q_len ? decay * mass[b][h_kv][k] : 0)
+ *                      + sum of w over the last last_q new tokens (0: all) and the G query
+ *                        heads of h_kv
+ * for k < kv_len; entries past it keep what they held.  mass fp32
+ * [B][H_kv][pages_per_seq * P]; decay >= 0 (0: old masses are not read).  The result does
+ * not depend on timing (no atomics). */
+cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_params_t* score,
+                                  const void* q, int64_t q_stride, const void* k_pool,
+                                  const int32_t* page_table, const int32_t* cu_q,
+                                  const int32_t* kv_len, const float* lse, int32_t last_q,
+                                  float decay, float* mass, cosa_stream_t stream);
+
+typedef struct {
+  int32_t budget; /* keys kept of each sequence and KV head, >= 1                        */
+  int32_t sink;   /* leading keys always kept, >= 0                                      */
+  int32_t recent; /* trailing keys always kept, >= 0; sink + recent <= budget            */
+} cosa_evict_params_t;
+
+/* Cut every sequence's cache to n' = min(kv_len, budget) keys a KV head: the sink and
+ * recent keys and, of the others, those with the largest mass (equal masses: the lower
+ * position first; a NaN mass counts as the lowest).  The kept keys stay in order: kept
+ * int32 [B][H_kv][budget] lists their positions ascending, -1 past n', and K, V of kept[j]
+ * are copied to slot j of the sequence's new pages dst_table int32
+ * [B][ceil(budget / P)] (physical pages of the same pools that page_table does not name
+ * and no other sequence of the call is given; the old pages stay as they were, so pages
+ * shared with other sequences are safe).  mass_out fp32 [B][H_kv][ceil(budget / P) * P]
+ * (may be NULL) gets the kept keys' masses, new_len int32 [B] (may be kv_len itself) n'.
+ * mass as for cosa_attention_mass.  shape's num_q_heads, total_q and max_q play no part
+ * beyond their checks; a kv_len outside [0, max_kv] is recorded as COSA_ERR_INVALID_ARG in
+ * the status word and the sequence left out. */
+cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_params_t* evict,
+                               void* k_pool, void* v_pool, const int32_t* page_table,
+                               const int32_t* kv_len, const float* mass,
+                               const int32_t* dst_table, int32_t* kept, int32_t* new_len,
+                               float* mass_out, cosa_stream_t stream);
+
 /* Read (and clear) the current device's status word: COSA_OK, or the first
  * in-kernel error recorded since the last call (e.g. COSA_ERR_TIMEOUT).
  * Synchronises `stream`. */
