@@ -190,9 +190,9 @@ struct ChunkCfg {
   static constexpr uint32_t OFF_K = OFF_Q + NT * Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + KS * BLK_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_V + VS * BLK_BYTES;
-  // q full / empty, k full / empty, v full / empty, v tail, s full[2], p full[2],
-  // o full[2], pv done, done
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 6 + 2;
+  // q full / empty, k full / empty, v full / empty, v tail, s full[2],
+  // p full[2][half], o full[2], pv done, done
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 8 + 2;
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBAR * 8 + 15) & ~15u;
   static constexpr uint32_t SMEM = OFF_MISC + 32;   // TMEM address, abort, start tile
   static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
@@ -232,6 +232,38 @@ struct ChunkWalk {
   }
 };
 
+// The waiting itself, kept out of line: two dozen inlined copies of these loops would not
+// leave the instruction cache room for the loops that work.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at,
+                                     unsigned long long tmo) {
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (tc::ld_shared_volatile(abort_at)) return false;
+    if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
+      tc::st_shared_volatile(abort_at, 1u);
+      set_status(COSA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __noinline__ bool wait_on_hot(uint32_t bar, uint32_t parity, uint32_t abort_at,
+                                         unsigned long long tmo) {
+  const uint64_t t0 = tc::globaltimer_ns();
+  uint32_t n = 0;
+  while (!tc::mbar_test_wait(bar, parity)) {
+    if ((++n & 255u) == 0) {
+      if (tc::ld_shared_volatile(abort_at)) return false;
+      if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
+        tc::st_shared_volatile(abort_at, 1u);
+        set_status(COSA_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 template <int D, int NT, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(128 + 128 * NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -253,14 +285,15 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   constexpr int B0 = 2 + 2 * C::KS + 2 * C::VS;
   const uint32_t b_vtail = bar + 8u * B0;
   auto b_sfull = [&](int i) { return bar + 8u * (B0 + 1 + i); };
-  auto b_pfull = [&](int i) { return bar + 8u * (B0 + 3 + i); };
-  auto b_ofull = [&](int i) { return bar + 8u * (B0 + 5 + i); };
-  const uint32_t b_pv = bar + 8u * (B0 + 7), b_done = bar + 8u * (B0 + 8);
+  auto b_pfull = [&](int i, int h) { return bar + 8u * (B0 + 3 + 2 * i + h); };
+  auto b_ofull = [&](int i) { return bar + 8u * (B0 + 7 + i); };
+  const uint32_t b_pv = bar + 8u * (B0 + 9), b_done = bar + 8u * (B0 + 10);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sg + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 4);
   volatile int* start_tile = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 8);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler too
   if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) return;
   const int G = prm.group, TOK = prm.tile_tokens, P = prm.page_size;
 
@@ -272,7 +305,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     mbar_init(b_vtail, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sfull(i), 1);
-      mbar_init(b_pfull(i), 4);
+      mbar_init(b_pfull(i, 0), 4);
+      mbar_init(b_pfull(i, 1), 4);
       mbar_init(b_ofull(i), 1);
     }
     mbar_init(b_pv, 1);
@@ -290,7 +324,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // ---- this CTA's share of the plan
   pdl_wait();
@@ -313,22 +347,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   walk.t = *start_tile;
 
   const unsigned long long tmo = prm.timeout_ns;
-  auto give_up = [&]() {
-    *abort_flag = 1;
-    set_status(COSA_ERR_TIMEOUT);
-  };
-  // bounded wait on an mbarrier phase; false on timeout or abort
+  // bounded waits on an mbarrier phase; false on timeout or abort
+  const uint32_t abort_at = sb0 + C::OFF_MISC + 4;
   auto wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar_addr, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar_addr, parity)) {
-      if (*abort_flag) return false;
-      if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || globaltimer_ns() - t0 > tmo) {
-        give_up();
-        return false;
-      }
-    }
-    return true;
+    return mbar_try_wait(bar_addr, parity) || wait_on(bar_addr, parity, abort_at, tmo);
   };
   auto wait_warp = [&](uint32_t bar_addr, uint32_t parity) -> bool {
     int okl = 1;
@@ -337,26 +359,15 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   };
   // the same without suspending: for the hand-offs on the softmax / MMA cycle
   auto wait_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-    if (mbar_test_wait(bar_addr, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    uint32_t n = 0;
-    while (!mbar_test_wait(bar_addr, parity)) {
-      if ((++n & 255u) == 0) {
-        if (*abort_flag) return false;
-        if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || globaltimer_ns() - t0 > tmo) {
-          give_up();
-          return false;
-        }
-      }
-    }
-    return true;
+    return mbar_test_wait(bar_addr, parity) || wait_on_hot(bar_addr, parity, abort_at, tmo);
   };
   auto wait_warp_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
     int okl = 1;
     if (lane == 0) okl = wait_hot(bar_addr, parity) ? 1 : 0;
     return __shfl_sync(0xffffffffu, okl, 0) != 0;
   };
-  const int ppb = C::KB / P;  // pages a block, at most 8: one a lane
+  const int pshift = 31 - __clz(P);        // P is a power of two
+  const int ppb = C::KB >> pshift;         // pages a block, at most 8: one a lane
   // coordinate of page `lane` of block j (-1: outside the pool, read as zeros)
   auto page_coord = [&](int b, int hk, int j, int np) -> int {
     if (lane >= np) return 0;
@@ -367,8 +378,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     }
     return ph * prm.num_kv_heads + hk;
   };
-  auto blk_pages = [&](int kv, int j) { return min(ppb, (kv - j * C::KB + P - 1) / P); };
+  auto blk_pages = [&](int kv, int j) {
+    return min(ppb, (kv - j * C::KB + P - 1) >> pshift);
+  };
 
+  if (warp < 4) {
   if (warp == 0) {
     // ================= Q and K ========================================================
     int it = 0, seg = 0;
@@ -415,7 +429,15 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     // ================= V ==============================================================
     int it = 0, tails = 0;
     bool ok = true;
+    ChunkJoin jn;  // the tile that this share starts and does not finish
+    jn.ntok = jn.tok0 = jn.hk = jn.last = 0;
     for (; ok && walk.next(prm.tiles, prm.cum); walk.advance()) {
+      if (walk.part == 1) {
+        jn.tok0 = walk.tile.tok0;
+        jn.ntok = walk.tile.ntok;
+        jn.hk = walk.hk;
+        jn.last = (int)((walk.w + walk.tile.nb - 1) / quota);
+      }
       int cz = page_coord(walk.tile.b, walk.hk, walk.jb, blk_pages(walk.tile.kv, walk.jb));
       for (int j = 0; j < walk.nb; ++j, ++it) {
         const int s = it % C::VS, np = blk_pages(walk.tile.kv, walk.jb + j);
@@ -455,97 +477,109 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       if (!ok) break;
     }
     if (lane == 0) {
+      ChunkJoin* o = prm.joins + blockIdx.x;
+      o->ntok = jn.ntok;
+      o->tok0 = jn.tok0;
+      o->hk = jn.hk;
+      o->last = jn.last;
       const uint64_t t0 = globaltimer_ns();
       for (int x = max(0, it - C::VS); x < it; ++x)
         drain_wait(b_vfull(x % C::VS), (x / C::VS) & 1, t0, tmo);
       if (tails > 0) drain_wait(b_vtail, (tails - 1) & 1, t0, tmo);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ================= MMA issue ====================================================
-      constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, 0);
-      constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, 1);
-      const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sK, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sV, C::KB * 128, 1024);
-      // S buffer sb = Q tile i of this segment times the K block in slot s
-      auto qk = [&](int i, int sbuf, int s) {
-        const uint64_t dqi = dq + ((uint32_t)i * C::Q_BYTES >> 4);
-        const uint64_t dks = dk + ((uint32_t)s * C::BLK_BYTES >> 4);
+    // ================= MMA issue ======================================================
+    // The whole warp walks, one elected lane issues: with warp-uniform control flow the
+    // operands stay in uniform registers.  Issued from a branch that one lane takes, every
+    // MMA first moved its five operands there, and cost 85-140 cycles instead of 64.
+    const uint32_t lead = elect_one();
+    constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, 0);
+    constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, 1);
+    const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+    const uint64_t dk = smem_desc_sw128(sK, 16, 1024);
+    const uint64_t dv = smem_desc_sw128(sV, C::KB * 128, 1024);
+    // S buffer sbuf = Q tile i times the K block in slot s
+    auto qk = [&](int i, int sbuf, int s) {
+      uint64_t dqi = dq + ((uint32_t)i * C::Q_BYTES >> 4);
+      uint64_t dks = dk + ((uint32_t)s * C::BLK_BYTES >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16_ss(tmem + sbuf * 128, dqi + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                      dks + (((k >> 2) * (C::KB * 128) + (k & 3) * 32) >> 4), ID_QK,
-                      k > 0 ? 1u : 0u);
-        mma_commit(b_sfull(sbuf));
-      };
-      // O of tile i (+)= P in S buffer sbuf times the V block in slot s
-      auto pv = [&](int i, int sbuf, int s, int keys, bool first) {
-        const uint64_t dvs = dv + ((uint32_t)s * C::BLK_BYTES >> 4);
-        const int nk = min(C::KB, (keys + 15) & ~15) / 16;
-        for (int k = 0; k < nk; ++k)
-          mma_bf16_ts(tmem + C::COL_O + i * D, tmem + sbuf * 128 + k * 8, dvs + ((k * 16 * 128) >> 4),
-                      ID_PV, (!first || k > 0) ? 1u : 0u);
-      };
-      int it = 0, seg = 0, np[2] = {0, 0};  // blocks, segments, P hand-offs of each tile
-      bool ok = true;
-      for (; ok && walk.next(prm.tiles, prm.cum); walk.advance(), ++seg) {
-        const int nt = (NT == 2 && walk.tile.ntok > TOK) ? 2 : 1, nb = walk.nb;
-        auto keys = [&](int j) { return walk.tile.kv - (walk.jb + j) * C::KB; };
-        auto kslot_wait = [&](int x) { return wait(b_kfull(x % C::KS), (x / C::KS) & 1); };
-        if (!wait(b_qfull, seg & 1) || !kslot_wait(it)) { ok = false; break; }
-        tc_fence_after();
-        for (int i = 0; i < nt; ++i) qk(i, NT == 1 ? it & 1 : i, it % C::KS);
-        mma_commit(b_kempty(it % C::KS));
-        if (nb == 1) mma_commit(b_qempty);
-        for (int j = 0; j < nb; ++j, ++it) {
-          const int vs = it % C::VS;
-          if (NT == 1 && j + 1 < nb) {  // the next block's scores, under this block's softmax
-            if (!kslot_wait(it + 1)) { ok = false; break; }
-            tc_fence_after();
-            qk(0, (it + 1) & 1, (it + 1) % C::KS);
-            mma_commit(b_kempty((it + 1) % C::KS));
-            if (j + 2 == nb) mma_commit(b_qempty);
-          }
-          if (!wait(b_vfull(vs), (it / C::VS) & 1)) { ok = false; break; }
-          bool k_next = false;
-          for (int i = 0; i < nt; ++i) {
-            if (!wait_hot(NT == 1 ? b_pfull(it & 1) : b_pfull(i), (NT == 1 ? it >> 1 : np[i]) & 1)) {
-              ok = false;
-              break;
+      for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ss_if(lead, tmem + sbuf * 128, dqi + 2 * k, dks + 2 * k, ID_QK,
+                         (h > 0 || k > 0) ? 1u : 0u);
+        dqi += (128 * 128) >> 4;
+        dks += (C::KB * 128) >> 4;
+      }
+      mma_commit_if(lead, b_sfull(sbuf));
+    };
+    int it = 0, seg = 0, cnt1 = 0;  // blocks of the CTA (and tile 0), segments, blocks of tile 1
+    bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+    auto kwait = [&](int x) { return all(wait(b_kfull(x % C::KS), (x / C::KS) & 1)); };
+    for (; ok; ++seg) {
+      if (!all(walk.next(prm.tiles, prm.cum))) break;
+      const int nb = __shfl_sync(0xffffffffu, walk.nb, 0);
+      const int keys0 = __shfl_sync(0xffffffffu, walk.tile.kv - walk.jb * C::KB, 0);
+      const int nt = NT == 2 && all(walk.tile.ntok > TOK) ? 2 : 1;
+      if (!all(wait(b_qfull, seg & 1))) { ok = false; break; }
+      // Step j: the products P V of block j - 1 and Q K^T of block j, in the order
+      //   NT = 2:  PV0(j-1) QK0(j) | PV1(j-1) QK1(j)
+      //   NT = 1:  QK(j) | PV(j-1), the scores under the softmax of the block before
+      for (int j = 0; j <= nb; ++j) {
+        const int vs = (it + j - 1 + C::VS) % C::VS, ks = (it + j) % C::KS;
+        if (j < nb) {
+          if (!kwait(it + j)) { ok = false; break; }
+          tc_fence_after();
+        }
+        if (NT == 1 && j < nb) qk(0, (it + j) & 1, ks);
+        if (j > 0 && !all(wait(b_vfull(vs), ((it + j - 1) / C::VS) & 1))) { ok = false; break; }
+        const int keys = keys0 - (j - 1) * C::KB;
+        // one copy for both tiles: the issue loop has to stay in the instruction cache, but its
+        // steps want to be unrolled (chunk of 2048 on 32K keys: 1.08 ms so, 1.16 ms with both
+        // tiles unrolled, 1.21 ms with the steps rolled)
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+          if (j > 0) {
+            const int sbuf = NT == 1 ? (it + j - 1) & 1 : i;
+            const uint32_t ph = (NT == 1 ? (it + j - 1) >> 1 : (i == 0 ? it + j - 1 : cnt1)) & 1;
+            uint64_t dvs = dv + ((uint32_t)vs * C::BLK_BYTES >> 4);
+            uint32_t t_p = tmem + sbuf * 128;
+            // O of tile i (+)= P V, 64 keys as soon as their P is there
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!all(wait_hot(b_pfull(sbuf, h), ph))) { ok = false; break; }
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ts_if(h * 64 + k * 16 < keys ? lead : 0u, tmem + C::COL_O + i * D,
+                               t_p + k * 8, dvs + ((k * 16 * 128) >> 4), ID_PV,
+                               (j > 1 || h > 0 || k > 0) ? 1u : 0u);
+              dvs += (64 * 128) >> 4;
+              t_p += 32;
             }
-            ++np[i];
-            tc_fence_after();
-            pv(i, NT == 1 ? it & 1 : i, vs, keys(j), j == 0);
-            if (NT == 1) {
-              mma_commit(b_pv);
-              if (j + 1 == nb) mma_commit(b_ofull(0));
-            } else if (j + 1 < nb) {
-              if (!k_next) {
-                if (!kslot_wait(it + 1)) { ok = false; break; }
-                tc_fence_after();
-                k_next = true;
-              }
-              qk(i, i, (it + 1) % C::KS);
-              if (i + 1 == nt) {
-                mma_commit(b_kempty((it + 1) % C::KS));
-                if (j + 2 == nb) mma_commit(b_qempty);
-              }
-            } else {
-              mma_commit(b_ofull(i));
-            }
+            if (!ok) break;
+            if (i == 1) ++cnt1;
+            if (NT == 1) mma_commit_if(lead, b_pv);
+            if (j == nb) mma_commit_if(lead, b_ofull(i));
           }
-          if (!ok) break;
-          mma_commit(b_vempty(vs));
+          if (NT == 2 && j < nb) qk(i, i, ks);
         }
         if (!ok) break;
+        if (j > 0) mma_commit_if(lead, b_vempty(vs));
+        if (j < nb) mma_commit_if(lead, b_kempty(ks));
+        if (j == nb - 1) mma_commit_if(lead, b_qempty);
       }
-      // every issued MMA completes before teardown frees TMEM
-      mma_commit(b_done);
-      const uint64_t t0 = globaltimer_ns();
-      drain_wait(b_done, 0, t0, tmo);
+      if (!ok) break;
+      it += nb;
+      walk.advance();
     }
-  } else if (warp >= 4) {
+    // every issued MMA completes before teardown frees TMEM
+    mma_commit_if(lead, b_done);
+    const uint64_t t0 = globaltimer_ns();
+    if (lane == 0) drain_wait(b_done, 0, t0, tmo);
+  }
+  } else {
     // ================= softmax of tile i, one row per thread ==========================
     const int i = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16);
@@ -576,102 +610,140 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         const int key0 = (walk.jb + j) * C::KB;
         // rows without a token never need the mask: their result goes nowhere
         const bool inside = !row_valid || (lo <= key0 && hi >= key0 + C::KB - 1);
-        if (warp_works) {
-          float rs[4] = {0.f, 0.f, 0.f, 0.f};
-          auto block = [&](auto mask_tag) {
-            constexpr bool MASK = decltype(mask_tag)::value;
-            const int rlo = lo - key0, rhi = hi - key0;
-            const float dist0 = (float)(key0 - pos);
-            auto seen = [&](int e) { return !MASK || (e >= rlo && e <= rhi); };
-            // score in log2 units
-            auto val = [&](uint32_t v, int e) {
-              float x = score_log2<CAP>(prm.score, __uint_as_float(v));
-              if (BIAS) x = fmaf(-slope, fabsf(dist0 + (float)e), x);
-              return seen(e) ? x : -INFINITY;
-            };
-            // for the row max, without a bias: the raw product (the cap is monotone)
-            auto raw = [&](uint32_t v, int e) {
-              if (BIAS) return val(v, e);
-              return seen(e) ? __uint_as_float(v) : -INFINITY;
-            };
-            float m_loc;
-            {
-              uint32_t sa[64], sb[64];
-              tmem_ld64_async(t_s, sa);
-              tmem_ld64_async(t_s + 64, sb);
-              tmem_ld_wait64x2(sa, sb);
-              float a[8];
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                a[e & 7] = e < 8 ? raw(sa[e], e) : fmaxf(a[e & 7], raw(sa[e], e));
-#pragma unroll
-              for (int e = 0; e < 64; ++e) a[e & 7] = fmaxf(a[e & 7], raw(sb[e], 64 + e));
-#pragma unroll
-              for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-                for (int e = 0; e < w; ++e) a[e] = fmaxf(a[e], a[e + w]);
-              m_loc = a[0];
-              if (!BIAS && m_loc != -INFINITY) m_loc = score_log2<CAP>(prm.score, m_loc);
-            }
-            const bool resc = m_loc > m_ref + C::kRescale;
-            if (j > 0 && __any_sync(0xffffffffu, resc)) {
-              if (NT == 1) {  // O is at rest once the previous block's product is done
-                if (!wait_warp(b_pv, (cnt - 1) & 1)) return false;
-                tc_fence_after();
-              }
-              const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
-#pragma unroll 1
-              for (int k = 0; k < D / 32; ++k) {
-                uint32_t r[32];
-                tmem_ld32(t_o + k * 32, r);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                tmem_st32(t_o + k * 32, r);
-              }
-              tmem_st_wait();
-              l *= alpha;
-            }
-            if (resc) m_ref = m_loc;
-            const float nb2 = m_ref == -INFINITY ? 0.f : -m_ref;
-            uint32_t va[32], vb[32], w[16];
-            tmem_ld32_async(t_s, va);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t* cur = (c & 1) ? vb : va;
-              uint32_t* nxt = (c & 1) ? va : vb;
-              tmem_ld_wait32(cur);
-              if (c < 3) tmem_ld32_async(t_s + (c + 1) * 32, nxt);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int x = c * 32 + 2 * e;
-                float x0, x1;
-                if (!CAP && !BIAS) {
-                  x0 = seen(x) ? fmaf(__uint_as_float(cur[2 * e]), prm.score.a, nb2) : -INFINITY;
-                  x1 = seen(x + 1) ? fmaf(__uint_as_float(cur[2 * e + 1]), prm.score.a, nb2)
-                                   : -INFINITY;
-                } else {
-                  x0 = val(cur[2 * e], x) + nb2;
-                  x1 = val(cur[2 * e + 1], x + 1) + nb2;
-                }
-                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                rs[e & 3] += p0;
-                rs[(e + 2) & 3] += p1;
-                __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
-                w[e] = *reinterpret_cast<uint32_t*>(&v2);
-              }
-              tmem_st16(t_s + c * 16, w);
-            }
-            return true;
-          };
-          ok = __all_sync(0xffffffffu, inside) ? block(std::false_type{}) : block(std::true_type{});
-          l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
         // one barrier a buffer: with one tile a warp without rows may be a block ahead of the
         // others, and its arrival must not count for theirs
-        if (lane == 0) mbar_arrive(b_pfull(sbuf));
+        auto hand_over = [&](int h) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_pfull(sbuf, h));
+        };
+        if (warp_works) {
+          const float dist0 = (float)(key0 - pos);
+          const bool whole_block = __all_sync(0xffffffffu, inside);
+          const int rlo = lo - key0, rhi = hi - key0;
+          // score in log2 units of column e (unseen keys: -inf)
+          auto val = [&](uint32_t v, int e) {
+            float x = score_log2<CAP>(prm.score, __uint_as_float(v));
+            if (BIAS) x = fmaf(-slope, fabsf(dist0 + (float)e), x);
+            return x;
+          };
+          // ---- row max.  Without a bias the cap and the scale are monotone: raw products do
+          float m_loc;
+          if (!BIAS && whole_block) {
+            uint32_t sa[64], sb[64];
+            tmem_ld64_async(t_s, sa);
+            tmem_ld64_async(t_s + 64, sb);
+            tmem_ld_wait64x2(sa, sb);
+            float a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              a[e] = fmaxf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
+#pragma unroll
+            for (int e = 8; e < 64; e += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                a[x] = fmax3f(a[x], __uint_as_float(sa[e + 2 * x]), __uint_as_float(sa[e + 2 * x + 1]));
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                a[x] = fmax3f(a[x], __uint_as_float(sb[e + 2 * x]), __uint_as_float(sb[e + 2 * x + 1]));
+            m_loc = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+            m_loc = score_log2<CAP>(prm.score, m_loc);
+          } else {
+            m_loc = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(t_s + c, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = BIAS ? val(v[e], c + e) : __uint_as_float(v[e]);
+                if (c + e >= rlo && c + e <= rhi) m_loc = fmaxf(m_loc, x);
+              }
+            }
+            if (!BIAS && m_loc != -INFINITY) m_loc = score_log2<CAP>(prm.score, m_loc);
+          }
+          const bool resc = m_loc > m_ref + C::kRescale;
+          if (j > 0 && __any_sync(0xffffffffu, resc)) {
+            if (NT == 1) {  // O is at rest once the previous block's product is done
+              if (!wait_warp(b_pv, (cnt - 1) & 1)) { ok = false; break; }
+              tc_fence_after();
+            }
+            const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t r[16];
+              tmem_ld16(t_o + k * 16, r);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st16(t_o + k * 16, r);
+            }
+            tmem_st_wait();
+            l *= alpha;
+          }
+          if (resc) m_ref = m_loc;
+          const float nb2 = m_ref == -INFINITY ? 0.f : -m_ref;
+          // ---- P = 2^(score - m_ref) as bf16 pairs over the first half of the S columns,
+          // handed to the MMA thread 64 keys at a time.  A rolled loop that reads S again: the
+          // SM's instruction cache holds all roles' loops only if this one is short (unrolled
+          // over a row held in registers, it missed 22 lines a block and ran a third slower)
+          const f32x2 mul2 = pack2(prm.score.a, prm.score.a), nb22 = pack2(nb2, nb2);
+          f32x2 sum[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = pack2(0.f, 0.f);
+          auto piece = [&](auto mask_tag, const uint32_t* v, int c) {  // 32 keys from column c
+            constexpr bool MASK = decltype(mask_tag)::value;
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              f32x2 x;
+              if (CAP || BIAS)
+                x = add2(pack2(val(v[2 * e], c + 2 * e), val(v[2 * e + 1], c + 2 * e + 1)), nb22);
+              else
+                x = fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), mul2, nb22);
+              float x0, x1;
+              unpack2(x, x0, x1);
+              if (MASK) {
+                if (c + 2 * e < rlo || c + 2 * e > rhi) x0 = -INFINITY;
+                if (c + 2 * e + 1 < rlo || c + 2 * e + 1 > rhi) x1 = -INFINITY;
+              }
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
+              __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+              w[e] = *reinterpret_cast<uint32_t*>(&v2);
+            }
+            tmem_st16(t_s + (c >> 1), w);
+          };
+          auto weights = [&](auto mask_tag) {
+            uint32_t va[32], vb[32];
+            tmem_ld32_async(t_s, va);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tmem_ld_wait32(va);
+              tmem_ld32_async(t_s + c + 32, vb);
+              piece(mask_tag, va, c);
+              if (c) {  // the first half's stores have had a quarter's time to land
+                tmem_st_wait();
+                hand_over(0);
+              }
+              tmem_ld_wait32(vb);
+              if (!c) tmem_ld32_async(t_s + 64, va);
+              piece(mask_tag, vb, c + 32);
+            }
+          };
+          if (whole_block) weights(std::false_type{});
+          else weights(std::true_type{});
+          tmem_st_wait();
+          hand_over(1);
+          const f32x2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          float t0, t1;
+          unpack2(t, t0, t1);
+          l += t0 + t1;
+        } else {
+          hand_over(0);
+          hand_over(1);
+        }
         if (!ok) break;
       }
       // ---- epilogue: O / l, or the partial rows of a tile cut between CTAs
@@ -718,26 +790,6 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         }
       }
       tc_fence_before();
-    }
-  } else if (warp == 3) {
-    // ================= the join list ==================================================
-    ChunkJoin jn;
-    jn.ntok = jn.tok0 = jn.hk = jn.last = 0;
-    while (walk.next(prm.tiles, prm.cum)) {
-      if (walk.part == 1) {
-        jn.tok0 = walk.tile.tok0;
-        jn.ntok = walk.tile.ntok;
-        jn.hk = walk.hk;
-        jn.last = (int)((walk.w + walk.tile.nb - 1) / quota);
-      }
-      walk.advance();
-    }
-    if (lane == 0) {
-      ChunkJoin* o = prm.joins + blockIdx.x;
-      o->tok0 = jn.tok0;
-      o->ntok = jn.ntok;
-      o->hk = jn.hk;
-      o->last = jn.last;
     }
   }
 
