@@ -618,50 +618,80 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           if (lane == 0) mbar_arrive(b_pfull(sbuf, h));
         };
         if (warp_works) {
-          const float dist0 = (float)(key0 - pos);
           const bool whole_block = __all_sync(0xffffffffu, inside);
           const int rlo = lo - key0, rhi = hi - key0;
-          // score in log2 units of column e (unseen keys: -inf)
-          auto val = [&](uint32_t v, int e) {
-            float x = score_log2<CAP>(prm.score, __uint_as_float(v));
-            if (BIAS) x = fmaf(-slope, fabsf(dist0 + (float)e), x);
+          const float dist0 = (float)(key0 - pos);
+          // scores of columns c + 2e, c + 2e + 1 in log2 units, plus `add`
+          auto pair = [&](auto small_tag, const uint32_t* v, int c, int e, f32x2 add) -> f32x2 {
+            f32x2 x = score2_log2<CAP, decltype(small_tag)::value>(
+                prm.score, pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), add);
+            if (BIAS) {
+              float d0, d1;
+              unpack2(add2(both(dist0 + (float)c), pack2((float)(2 * e), (float)(2 * e + 1))), d0, d1);
+              x = fma2(both(-slope), pack2(fabsf(d0), fabsf(d1)), x);
+            }
             return x;
           };
+          // one bit a column of [c, c + 32): seen
+          auto seen_bits = [&](int c) -> uint32_t {
+            const int b0 = max(rlo - c, 0), b1 = min(rhi - c, 31);
+            return b0 > b1 ? 0u : (0xffffffffu << b0) & (0xffffffffu >> (31 - b1));
+          };
+          // f(v, c) for the row's columns, 32 at a time, the next ones loading meanwhile
+          auto pieces = [&](auto f) {
+            uint32_t va[32], vb[32];
+            tmem_ld32_async(t_s, va);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tmem_ld_wait32(va);
+              tmem_ld32_async(t_s + c + 32, vb);
+              f(va, c);
+              tmem_ld_wait32(vb);
+              if (!c) tmem_ld32_async(t_s + 64, va);
+              f(vb, c + 32);
+            }
+          };
           // ---- row max.  Without a bias the cap and the scale are monotone: raw products do
-          float m_loc;
+          float m_loc, far = 0.f;  // far: the largest |product| seen (capped scores)
           if (!BIAS && whole_block) {
             uint32_t sa[64], sb[64];
             tmem_ld64_async(t_s, sa);
             tmem_ld64_async(t_s + 64, sb);
             tmem_ld_wait64x2(sa, sb);
-            float a[4];
+            float a[4], z[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
               a[e] = fmaxf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
+              if (CAP) z[e] = fminf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
+            }
 #pragma unroll
-            for (int e = 8; e < 64; e += 8)
+            for (int e = 8; e < 128; e += 8)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                a[x] = fmax3f(a[x], __uint_as_float(sa[e + 2 * x]), __uint_as_float(sa[e + 2 * x + 1]));
-#pragma unroll
-            for (int e = 0; e < 64; e += 8)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                a[x] = fmax3f(a[x], __uint_as_float(sb[e + 2 * x]), __uint_as_float(sb[e + 2 * x + 1]));
+              for (int x = 0; x < 4; ++x) {
+                const float u = __uint_as_float(e < 64 ? sa[e + 2 * x] : sb[e - 64 + 2 * x]);
+                const float w = __uint_as_float(e < 64 ? sa[e + 2 * x + 1] : sb[e - 64 + 2 * x + 1]);
+                a[x] = fmax3f(a[x], u, w);
+                if (CAP) z[x] = fmin3f(z[x], u, w);
+              }
             m_loc = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+            if (CAP) far = fmaxf(fabsf(m_loc), fabsf(fminf(fminf(z[0], z[1]), fminf(z[2], z[3]))));
             m_loc = score_log2<CAP>(prm.score, m_loc);
           } else {
-            m_loc = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(t_s + c, v);
+            float a[2] = {-INFINITY, -INFINITY};
+            pieces([&](const uint32_t* v, int c) {
+              const uint32_t bits = whole_block ? 0xffffffffu : seen_bits(c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = BIAS ? val(v[e], c + e) : __uint_as_float(v[e]);
-                if (c + e >= rlo && c + e <= rhi) m_loc = fmaxf(m_loc, x);
+              for (int e = 0; e < 16; ++e) {
+                float x0 = __uint_as_float(v[2 * e]), x1 = __uint_as_float(v[2 * e + 1]);
+                if (CAP) far = fmaxf(far, fmaxf((bits >> (2 * e)) & 1u ? fabsf(x0) : 0.f,
+                                                (bits >> (2 * e + 1)) & 1u ? fabsf(x1) : 0.f));
+                if (BIAS) unpack2(pair(std::false_type{}, v, c, e, both(0.f)), x0, x1);
+                if (!((bits >> (2 * e)) & 1u)) x0 = -INFINITY;
+                if (!((bits >> (2 * e + 1)) & 1u)) x1 = -INFINITY;
+                a[e & 1] = fmax3f(a[e & 1], x0, x1);
               }
-            }
+            });
+            m_loc = fmaxf(a[0], a[1]);
             if (!BIAS && m_loc != -INFINITY) m_loc = score_log2<CAP>(prm.score, m_loc);
           }
           const bool resc = m_loc > m_ref + C::kRescale;
@@ -688,52 +718,43 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           // handed to the MMA thread 64 keys at a time.  A rolled loop that reads S again: the
           // SM's instruction cache holds all roles' loops only if this one is short (unrolled
           // over a row held in registers, it missed 22 lines a block and ran a third slower)
-          const f32x2 mul2 = pack2(prm.score.a, prm.score.a), nb22 = pack2(nb2, nb2);
+          const f32x2 nb22 = both(nb2);
           f32x2 sum[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = pack2(0.f, 0.f);
-          auto piece = [&](auto mask_tag, const uint32_t* v, int c) {  // 32 keys from column c
-            constexpr bool MASK = decltype(mask_tag)::value;
-            uint32_t w[16];
+          for (int e = 0; e < 4; ++e) sum[e] = both(0.f);
+          auto weights = [&](auto mask_tag, auto small_tag) {
+            pieces([&](const uint32_t* v, int c) {
+              constexpr bool MASK = decltype(mask_tag)::value;
+              const uint32_t bits = MASK ? seen_bits(c) : 0u;
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              f32x2 x;
-              if (CAP || BIAS)
-                x = add2(pack2(val(v[2 * e], c + 2 * e), val(v[2 * e + 1], c + 2 * e + 1)), nb22);
-              else
-                x = fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), mul2, nb22);
-              float x0, x1;
-              unpack2(x, x0, x1);
-              if (MASK) {
-                if (c + 2 * e < rlo || c + 2 * e > rhi) x0 = -INFINITY;
-                if (c + 2 * e + 1 < rlo || c + 2 * e + 1 > rhi) x1 = -INFINITY;
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                unpack2(pair(small_tag, v, c, e, nb22), x0, x1);
+                if (MASK) {
+                  if (!((bits >> (2 * e)) & 1u)) x0 = -INFINITY;
+                  if (!((bits >> (2 * e + 1)) & 1u)) x1 = -INFINITY;
+                }
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
+                __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+                w[e] = *reinterpret_cast<uint32_t*>(&v2);
               }
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
-              __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
-              w[e] = *reinterpret_cast<uint32_t*>(&v2);
-            }
-            tmem_st16(t_s + (c >> 1), w);
-          };
-          auto weights = [&](auto mask_tag) {
-            uint32_t va[32], vb[32];
-            tmem_ld32_async(t_s, va);
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
-              tmem_ld_wait32(va);
-              tmem_ld32_async(t_s + c + 32, vb);
-              piece(mask_tag, va, c);
-              if (c) {  // the first half's stores have had a quarter's time to land
+              tmem_st16(t_s + (c >> 1), w);
+              if (c == 64) {  // the first half's stores have had a quarter's time to land
                 tmem_st_wait();
                 hand_over(0);
               }
-              tmem_ld_wait32(vb);
-              if (!c) tmem_ld32_async(t_s + 64, va);
-              piece(mask_tag, vb, c + 32);
-            }
+            });
           };
-          if (whole_block) weights(std::false_type{});
-          else weights(std::true_type{});
+          const bool small = CAP && __all_sync(0xffffffffu, !row_valid || far <= prm.score.lim);
+          if (whole_block) {
+            if (small) weights(std::false_type{}, std::true_type{});
+            else weights(std::false_type{}, std::false_type{});
+          } else {
+            if (small) weights(std::true_type{}, std::true_type{});
+            else weights(std::true_type{}, std::false_type{});
+          }
           tmem_st_wait();
           hand_over(1);
           const f32x2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));

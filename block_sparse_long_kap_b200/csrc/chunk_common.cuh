@@ -53,28 +53,6 @@ __device__ __forceinline__ void token_range(const ChunkMask& m, int token, int p
   hi = min(max(pos, prefix - 1), kv - 1);
 }
 
-// Score in log2 units from the raw product.  Plain: raw * a.  Capped:
-// c tanh(raw * scale / c) = c - 2c / (1 + e^(2 raw scale / c)), with the exponential and
-// the reciprocal on the special-function unit: absolute error about c * 2^-23, where the
-// hardware tanh (relative error 2^-11) would move a logit near a cap of 50 by 0.02.
-struct ScoreShape {
-  float a;      // plain: scale * log2 e; capped: 2 * scale / c * log2 e
-  float cap2;   // c * log2 e
-};
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <bool CAP>
-__device__ __forceinline__ float score_log2(const ScoreShape& s, float raw) {
-  if (!CAP) return raw * s.a;
-  const float r = rcp_approx(1.f + tc::ex2_approx(raw * s.a));
-  return fmaf(-2.f * s.cap2, r, s.cap2);
-}
-
 // Pairs of floats in one 64-bit register: the FMA pipe takes both in one instruction.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -95,28 +73,55 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pack2(a, a); }
 
-// 2^x of a pair on the FMA pipe, for x <= 127: x = n + f with n the nearest integer (taken
-// from the low mantissa bits of x + 1.5 * 2^23, after Cody and Waite), 2^f on [-1/2, 1/2] by
-// a degree-4 polynomial of least relative error (2.6e-6, far below the 2^-9 of the bf16
-// weights), n added to the exponent.  x below -126 gives 2^-126.
-__device__ __forceinline__ f32x2 exp2_poly2(f32x2 x) {
-  float x0, x1;
-  unpack2(x, x0, x1);
-  x = pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const f32x2 magic = pack2(12582912.f, 12582912.f), neg = pack2(-12582912.f, -12582912.f);
-  const f32x2 t = add2(x, magic);
-  const f32x2 f = fma2(add2(t, neg), pack2(-1.f, -1.f), x);
-  f32x2 p = pack2(0.00957010179f, 0.00957010179f);
-  p = fma2(p, f, pack2(0.0559178603f, 0.0559178603f));
-  p = fma2(p, f, pack2(0.240247448f, 0.240247448f));
-  p = fma2(p, f, pack2(0.693121815f, 0.693121815f));
-  p = fma2(p, f, pack2(0.999999261f, 0.999999261f));
-  float t0, t1, p0, p1;
-  unpack2(t, t0, t1);
-  unpack2(p, p0, p1);
-  return pack2(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
-               __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)));
+// Scores in log2 units from raw products.  Plain: raw * a.  Capped: with y = raw * scale / c,
+//   c tanh(y) = c - 2c / (1 + e^2y),
+// the exponential and the reciprocal on the special-function unit: absolute error about
+// c * 2^-23, where the hardware tanh (relative error 2^-11) would move a logit near a cap of
+// 50 by 0.02.  While |y| <= 0.625 (logits well inside the cap, the usual case) an odd
+// polynomial of degree 9 does (least absolute error on that range, 4.3e-8), on the FMA pipe:
+// two special-function results less an element, of three.
+struct ScoreShape {
+  float a;    // scale * log2 e
+  float e2;   // capped: 2 * scale / c * log2 e
+  float cap;  // capped: c * log2 e
+  float y;    // capped: scale / c
+  float lim;  // capped: the raw product at y = 0.625
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool CAP>
+__device__ __forceinline__ float score_log2(const ScoreShape& s, float raw) {
+  if (!CAP) return raw * s.a;
+  const float r = rcp_approx(1.f + tc::ex2_approx(raw * s.e2));
+  return fmaf(-2.f * s.cap, r, s.cap);
+}
+
+// A pair of scores in log2 units plus `add`; SMALL: both products are within s.lim.
+template <bool CAP, bool SMALL>
+__device__ __forceinline__ f32x2 score2_log2(const ScoreShape& s, f32x2 raw, f32x2 add) {
+  if (!CAP) return fma2(raw, both(s.a), add);
+  if (SMALL) {  // y + y z q(z), z = y^2, scaled by c log2 e
+    const f32x2 y = mul2(raw, both(s.y)), z = mul2(y, y);
+    f32x2 q = fma2(z, both(0.0148892366f), both(-0.0517016767f));
+    q = fma2(q, z, both(0.133020084f));
+    q = fma2(q, z, both(-0.333318751f));
+    return fma2(mul2(raw, both(s.a)), mul2(q, z), fma2(raw, both(s.a), add));
+  }
+  float r0, r1;
+  unpack2(raw, r0, r1);
+  return add2(pack2(score_log2<true>(s, r0), score_log2<true>(s, r1)), add);
 }
 
 // Programmatic dependent launch: wait for the kernels before this one in the stream, and

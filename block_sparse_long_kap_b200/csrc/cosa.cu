@@ -465,11 +465,17 @@ ChunkMask chunk_mask(const cosa_score_params_t* s) {
 }
 
 ScoreShape score_shape(const cosa_chunk_t* s, const cosa_score_params_t* sc) {
-  const float log2e = 1.4426950408889634f;
-  if (sc && sc->softcap > 0.f)
-    return ScoreShape{(float)(2.0 * s->softmax_scale / sc->softcap * 1.4426950408889634),
-                      sc->softcap * log2e};
-  return ScoreShape{s->softmax_scale * log2e, 0.f};
+  const double log2e = 1.4426950408889634, scale = s->softmax_scale;
+  ScoreShape r;
+  std::memset(&r, 0, sizeof(r));
+  r.a = (float)(scale * log2e);
+  if (sc && sc->softcap > 0.f) {
+    r.e2 = (float)(2.0 * scale / sc->softcap * log2e);
+    r.cap = (float)(sc->softcap * log2e);
+    r.y = (float)(scale / sc->softcap);
+    r.lim = (float)(0.625 * sc->softcap / scale);
+  }
+  return r;
 }
 
 // bf16 [tokens][heads][D] with a token stride: box = 64 columns x G heads x `tokens` tokens
