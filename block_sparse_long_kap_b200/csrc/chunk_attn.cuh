@@ -232,38 +232,6 @@ struct ChunkWalk {
   }
 };
 
-// The waiting itself, kept out of line: two dozen inlined copies of these loops would not
-// leave the instruction cache room for the loops that work.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at,
-                                     unsigned long long tmo) {
-  const uint64_t t0 = tc::globaltimer_ns();
-  while (!tc::mbar_try_wait(bar, parity)) {
-    if (tc::ld_shared_volatile(abort_at)) return false;
-    if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
-      tc::st_shared_volatile(abort_at, 1u);
-      set_status(COSA_ERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __noinline__ bool wait_on_hot(uint32_t bar, uint32_t parity, uint32_t abort_at,
-                                         unsigned long long tmo) {
-  const uint64_t t0 = tc::globaltimer_ns();
-  uint32_t n = 0;
-  while (!tc::mbar_test_wait(bar, parity)) {
-    if ((++n & 255u) == 0) {
-      if (tc::ld_shared_volatile(abort_at)) return false;
-      if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
-        tc::st_shared_volatile(abort_at, 1u);
-        set_status(COSA_ERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-  return true;
-}
-
 template <int D, int NT, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(128 + 128 * NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,

@@ -10,7 +10,7 @@
 
 namespace cosa {
 
-constexpr int CHUNK_MAX_BATCH = 8192;
+constexpr int CHUNK_MAX_BATCH = 4096;
 constexpr int NUM_SMS = 148;  // B200
 
 struct ChunkSeqs {
@@ -122,6 +122,38 @@ __device__ __forceinline__ f32x2 score2_log2(const ScoreShape& s, f32x2 raw, f32
   float r0, r1;
   unpack2(raw, r0, r1);
   return add2(pack2(score_log2<true>(s, r0), score_log2<true>(s, r1)), add);
+}
+
+// The waiting itself, kept out of line: two dozen inlined copies of these loops would not
+// leave the instruction cache room for the loops that work.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at,
+                                     unsigned long long tmo) {
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (tc::ld_shared_volatile(abort_at)) return false;
+    if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
+      tc::st_shared_volatile(abort_at, 1u);
+      set_status(COSA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __noinline__ bool wait_on_hot(uint32_t bar, uint32_t parity, uint32_t abort_at,
+                                         unsigned long long tmo) {
+  const uint64_t t0 = tc::globaltimer_ns();
+  uint32_t n = 0;
+  while (!tc::mbar_test_wait(bar, parity)) {
+    if ((++n & 255u) == 0) {
+      if (tc::ld_shared_volatile(abort_at)) return false;
+      if (*(volatile int*)&g_status == COSA_ERR_TIMEOUT || tc::globaltimer_ns() - t0 > tmo) {
+        tc::st_shared_volatile(abort_at, 1u);
+        set_status(COSA_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 // Programmatic dependent launch: wait for the kernels before this one in the stream, and

@@ -479,14 +479,15 @@ ScoreShape score_shape(const cosa_chunk_t* s, const cosa_score_params_t* sc) {
 }
 
 // bf16 [tokens][heads][D] with a token stride: box = 64 columns x G heads x `tokens` tokens
-bool make_map_q(CUtensorMap* m, const void* base, const cosa_chunk_t* s, int64_t stride) {
+bool make_map_q(CUtensorMap* m, const void* base, const cosa_chunk_t* s, int64_t stride,
+                int tokens) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const int G = s->num_q_heads / s->num_kv_heads;
   cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_q_heads,
                         (cuuint64_t)s->total_q};
   cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)stride * 2};
-  cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)tokens};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -560,7 +561,8 @@ cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
   using Cfg = ChunkCfg<D, NT>;
   CUtensorMap mq, mk, mv;
   const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
-  if (!make_map_q(&mq, q, s, q_stride) || !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size) ||
+  if (!make_map_q(&mq, q, s, q_stride, prm.tile_tokens) ||
+      !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size) ||
       !make_map(&mv, v_pool, D, s->page_size, PZ, s->page_size))
     return COSA_ERR_CUDA;
   auto kern = chunk_attn_kernel<D, NT, CAP, BIAS>;
@@ -590,28 +592,29 @@ cosa_status_t launch_chunk_n(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
 
 template <int D, bool CAP, bool BIAS>
 cosa_status_t launch_mass_t(const cosa_chunk_t* s, const MassParams& prm, const void* q,
-                            int64_t q_stride, const void* k_pool, dim3 grid, cudaStream_t st) {
+                            int64_t q_stride, const void* k_pool, cudaStream_t st) {
   using Cfg = MassCfg<D>;
   CUtensorMap mq, mk;
   const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
-  if (!make_map_q(&mq, q, s, q_stride) || !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size))
+  if (!make_map_q(&mq, q, s, q_stride, prm.box_tokens) ||
+      !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size))
     return COSA_ERR_CUDA;
   auto kern = attn_mass_kernel<D, CAP, BIAS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Cfg::SMEM_ALLOC) != cudaSuccess)
+                           (int)Cfg::smem(CHUNK_MAX_BATCH)) != cudaSuccess)
     return COSA_ERR_CUDA;
-  kern<<<grid, Cfg::THREADS, Cfg::SMEM_ALLOC, st>>>(mq, mk, prm);
+  kern<<<NUM_SMS, Cfg::THREADS, Cfg::smem(s->batch), st>>>(mq, mk, prm);
   return last_launch();
 }
 
 template <int D>
 cosa_status_t launch_mass_d(const cosa_chunk_t* s, const MassParams& prm, bool cap, const void* q,
-                            int64_t q_stride, const void* k_pool, dim3 grid, cudaStream_t st) {
+                            int64_t q_stride, const void* k_pool, cudaStream_t st) {
   const bool bias = prm.slopes != nullptr;
-  if (cap && bias) return launch_mass_t<D, true, true>(s, prm, q, q_stride, k_pool, grid, st);
-  if (cap) return launch_mass_t<D, true, false>(s, prm, q, q_stride, k_pool, grid, st);
-  if (bias) return launch_mass_t<D, false, true>(s, prm, q, q_stride, k_pool, grid, st);
-  return launch_mass_t<D, false, false>(s, prm, q, q_stride, k_pool, grid, st);
+  if (cap && bias) return launch_mass_t<D, true, true>(s, prm, q, q_stride, k_pool, st);
+  if (cap) return launch_mass_t<D, true, false>(s, prm, q, q_stride, k_pool, st);
+  if (bias) return launch_mass_t<D, false, true>(s, prm, q, q_stride, k_pool, st);
+  return launch_mass_t<D, false, false>(s, prm, q, q_stride, k_pool, st);
 }
 
 // Test hook of cosa_debug_osk_wait_fault: one-shot, per host thread.
@@ -1329,7 +1332,6 @@ cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_pa
       !std::isfinite(decay))
     return COSA_ERR_INVALID_ARG;
   if (!good_stride(q_stride, shape->num_q_heads, shape->head_dim)) return COSA_ERR_INVALID_ARG;
-  if (shape->batch > 65535) return COSA_ERR_UNSUPPORTED;
   MassParams p;
   std::memset(&p, 0, sizeof(p));
   p.seqs = chunk_seqs(shape, cu_q, kv_len);
@@ -1347,22 +1349,17 @@ cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_pa
   p.num_phys_pages = shape->num_phys_pages;
   p.tile_tokens = 128 / p.group;
   p.last_q = last_q;
-  int rows = last_q > 0 && last_q < shape->max_q ? last_q : shape->max_q;
-  rows = (rows < p.tile_tokens ? rows : p.tile_tokens) * p.group;
-  p.cols = (rows + 15) / 16 * 16;
+  const int most = last_q > 0 && last_q < shape->max_q ? last_q : shape->max_q;
+  p.held = most <= 2 * p.tile_tokens;
+  p.box_tokens = most < p.tile_tokens ? most : p.tile_tokens;
+  p.cols = (p.box_tokens * p.group + 15) / 16 * 16;
   p.decay = decay;
   p.score = score_shape(shape, score);
   p.timeout_ns = kWaitTimeoutNs;
-  // runs of key blocks: enough for several CTAs an SM over the whole call
-  const long long bh = (long long)shape->batch * shape->num_kv_heads;
-  const long long nblk = ((long long)shape->max_kv + 127) / 128;
-  long long parts = (4 * NUM_SMS + bh - 1) / bh;
-  if (parts > nblk) parts = nblk;
-  dim3 grid((unsigned)parts, shape->num_kv_heads, shape->batch);
   const bool cap = score && score->softcap > 0.f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return shape->head_dim == 128 ? launch_mass_d<128>(shape, p, cap, q, q_stride, k_pool, grid, st)
-                                : launch_mass_d<64>(shape, p, cap, q, q_stride, k_pool, grid, st);
+  return shape->head_dim == 128 ? launch_mass_d<128>(shape, p, cap, q, q_stride, k_pool, st)
+                                : launch_mass_d<64>(shape, p, cap, q, q_stride, k_pool, st);
 }
 
 cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_params_t* evict,
@@ -1401,15 +1398,22 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   p.sink = evict->sink;
   p.recent = evict->recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<dim3(EVICT_CL, shape->num_kv_heads, shape->batch), EVICT_THREADS, 0, st>>>(p);
+  // the largest segment's keys, where they fit beside the static histograms
+  const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
+  p.seg_cap = seg <= EVICT_SEG_MAX ? seg : 0;
+  const size_t smem = (size_t)p.seg_cap * sizeof(uint32_t);
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           EVICT_SEG_MAX * (int)sizeof(uint32_t)) != cudaSuccess)
+    return COSA_ERR_CUDA;
+  evict_select_kernel<<<dim3(EVICT_CL, shape->num_kv_heads, shape->batch), EVICT_THREADS, smem,
+                        st>>>(p);
   e = last_launch();
   if (e != COSA_OK) return e;
   const int most = evict->budget < shape->max_kv ? evict->budget : shape->max_kv;
   const int rows = GATHER_THREADS / (shape->head_dim / 8) * GATHER_UNROLL;
   dim3 grid((most + rows - 1) / rows, shape->num_kv_heads, shape->batch);
-  if (shape->head_dim == 128) evict_gather_kernel<128><<<grid, GATHER_THREADS, 0, st>>>(p);
-  else evict_gather_kernel<64><<<grid, GATHER_THREADS, 0, st>>>(p);
-  return last_launch();
+  return launch_pdl(shape->head_dim == 128 ? evict_gather_kernel<128> : evict_gather_kernel<64>, grid,
+                    GATHER_THREADS, 0, st, p);
 }
 
 cosa_status_t cosa_get_status(cosa_stream_t stream) {

@@ -3,10 +3,12 @@
 // pages.
 //
 // evict_select_kernel: one cluster of 8 CTAs per (b, h_kv); each CTA owns a contiguous
-// eighth of the candidates.  The K-th largest mass is found by a radix select over the
-// order-preserving 32-bit form of the float (digits of 11, 11 and 10 bits: three passes
-// over the masses, which stay in L2), the eight histograms summed through distributed
-// shared memory.  Equal masses at the border go to the lowest positions: the CTAs' counts
+// eighth of the candidates and holds their keys in shared memory.  The K-th largest mass is
+// found by a radix select over the order-preserving 32-bit form of the float (digits of 11,
+// 11 and 10 bits); the CTAs add their histograms' non-empty bins into one that is spread
+// over the cluster's shared memories, one cluster barrier a digit (reading all eight
+// histograms instead cost 5,000 cycles a digit: distributed shared memory moves some 13
+// bytes a cycle).  Equal masses at the border go to the lowest positions: the CTAs' counts
 // of larger and of equal keys give each one its place, so the kept list comes out ascending
 // and is the same on every run.
 // evict_gather_kernel: a copy, 16 bytes a lane, source pages never written.
@@ -28,11 +30,14 @@ struct EvictParams {
   long long mass_stride;
   int num_kv_heads, page_size, pages_per_seq, num_phys_pages, max_kv, dst_pages;
   int budget, sink, recent;
+  int seg_cap;  // keys of a segment that the selection holds in shared memory
 };
 
 constexpr int EVICT_CL = 8;
 constexpr int EVICT_THREADS = 512;
 constexpr int EVICT_BINS = 2048;
+constexpr int EVICT_SLICE = EVICT_BINS / EVICT_CL;  // bins that a CTA sums
+constexpr int EVICT_SEG_MAX = 40960;  // keys of a segment in shared memory (160 KB)
 
 // Larger float, larger key; -0 is +0; a NaN is below everything.
 __device__ __forceinline__ uint32_t mass_key(float v) {
@@ -44,13 +49,38 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// word of another CTA of the cluster at the same shared-memory offset
+// its two halves: leaving the first means having come, the second waits for all
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// words of another CTA of the cluster at the same shared-memory offset
+__device__ __forceinline__ uint4 ld_cluster4(const void* p, int rank) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  uint32_t r;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_cluster(const void* p, int rank) {
   const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
   uint32_t r, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void add_cluster(const void* p, int rank, uint32_t v) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
 }
 
 // Exclusive prefix sum over the block; total gets the sum.  red: 32 words.
@@ -76,15 +106,21 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32
   return before + inc - v;
 }
 
+// Dynamic shared memory: the segment's keys, p.seg_cap words (0: they are read again from
+// the masses in every pass, for caches past 8 * 40960 keys).
 __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS)
     evict_select_kernel(const EvictParams p) {
-  __shared__ uint32_t hist[EVICT_BINS];
-  __shared__ uint32_t slice[EVICT_BINS / EVICT_CL];
+  extern __shared__ uint32_t keys_s[];
+  __shared__ __align__(16) uint32_t hist[3][EVICT_BINS];  // this CTA's counts of each digit
+  // the cluster's counts: this CTA's slice of the bins
+  __shared__ __align__(16) uint32_t sums[3][EVICT_SLICE];
   __shared__ uint32_t red[32];
   __shared__ uint32_t found[2];  // digit, keys above it
   __shared__ uint32_t cnt_s[2];  // this CTA's keys above / at the border
-  const int tid = threadIdx.x, rank = blockIdx.x;
+  __shared__ uint32_t warp_s[2][EVICT_THREADS / 32];
+  const int tid = threadIdx.x, rank = blockIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y, b = blockIdx.z;
+  pdl_launch();
   const int kv = __ldg(p.kv_len + b);
   if (kv < 0 || kv > p.max_kv) {
     if (tid == 0) set_status(COSA_ERR_INVALID_ARG);
@@ -103,44 +139,64 @@ __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS
   if (want == 0) return;
   const int m = kv - p.sink - p.recent;  // > want
   const int seg = (m + EVICT_CL - 1) / EVICT_CL;
-  const int s0 = min(rank * seg, m), s1 = min(s0 + seg, m);
-  const float* mass = p.mass + bh * p.mass_stride + p.sink;
+  const int s0 = min(rank * seg, m), n = min(s0 + seg, m) - s0;
+  const float* mass = p.mass + bh * p.mass_stride + p.sink + s0;
+  const bool held = seg <= p.seg_cap;
+  auto key = [&](int i) { return held ? keys_s[i] : mass_key(__ldg(mass + i)); };
+  for (int i = tid; i < 3 * EVICT_BINS / 4; i += EVICT_THREADS)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < 3 * EVICT_SLICE; i += EVICT_THREADS) sums[0][i] = 0u;
+  if (held) {
+    int i = tid;
+    for (; i + 7 * EVICT_THREADS < n; i += 8 * EVICT_THREADS) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __ldg(mass + i + e * EVICT_THREADS);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) keys_s[i + e * EVICT_THREADS] = mass_key(v[e]);
+    }
+    for (; i < n; i += EVICT_THREADS) keys_s[i] = mass_key(__ldg(mass + i));
+  }
+  cluster_sync();  // every CTA's sums are zero before any is added to
   uint32_t prefix = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < EVICT_BINS; i += EVICT_THREADS) hist[i] = 0;
+    for (int i0 = 0; i0 < n; i0 += EVICT_THREADS) {
+      const int i = i0 + tid;
+      const uint32_t k = i < n ? key(i) : 0u;
+      const bool in = i < n && (pass == 0 || (k >> (shift + bits)) == prefix);
+      // masses of exactly zero (keys that no token has seen) come in numbers: a warp counts
+      // its own with one addition
+      const uint32_t zero = __ballot_sync(0xffffffffu, in && k == 0x80000000u);
+      const bool mine = in && (k != 0x80000000u || lane == __ffs(zero) - 1);
+      if (mine)
+        atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1u)],
+                  k == 0x80000000u ? (uint32_t)__popc(zero) : 1u);
+    }
     __syncthreads();
-    for (int i = s0 + tid; i < s1; i += EVICT_THREADS) {
-      const uint32_t k = mass_key(__ldg(mass + i));
-      if (pass == 0 || (k >> (shift + bits)) == prefix)
-        atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-    }
-    cluster_sync();
-    // this CTA sums its eighth of the bins over the cluster
-    if (tid < EVICT_BINS / EVICT_CL) {
-      uint32_t t = 0;
-#pragma unroll
-      for (int r = 0; r < EVICT_CL; ++r) t += ld_cluster(&hist[rank * (EVICT_BINS / EVICT_CL) + tid], r);
-      slice[tid] = t;
-    }
+    // a thread's four bins into the slices that their owners hold; few are not empty
+    const int bin0 = EVICT_BINS - 4 - 4 * tid;
+    const uint4 h = *reinterpret_cast<const uint4*>(&hist[pass][bin0]);
+    uint32_t* at = &sums[pass][bin0 % EVICT_SLICE];
+    const int owner = bin0 / EVICT_SLICE;
+    if (h.x) add_cluster(at, owner, h.x);
+    if (h.y) add_cluster(at + 1, owner, h.y);
+    if (h.z) add_cluster(at + 2, owner, h.z);
+    if (h.w) add_cluster(at + 3, owner, h.w);
     cluster_sync();
     // from the largest digit down: the digit at which `want` keys are reached
-    uint32_t c[4], sum = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int bin = EVICT_BINS - 1 - (4 * tid + e);
-      c[e] = ld_cluster(&slice[bin % (EVICT_BINS / EVICT_CL)], bin / (EVICT_BINS / EVICT_CL));
-      sum += c[e];
-    }
+    const uint4 t4 = ld_cluster4(at, owner);
+    const uint32_t c[4] = {t4.w, t4.z, t4.y, t4.x};
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t total;
     uint32_t above = block_scan(sum, red, total);
     if (above < want && above + sum >= want) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (above < want && above + c[e] >= want) {
-          found[0] = EVICT_BINS - 1 - (4 * tid + e);
+          found[0] = bin0 + 3 - e;
           found[1] = above;
         }
         above += c[e];
@@ -149,52 +205,58 @@ __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS
     __syncthreads();
     prefix = (prefix << bits) | found[0];
     want -= found[1];
+    __syncthreads();
   }
-  // keys above the border value are kept, of the equal ones the first `want`
+  // keys above the border value are kept, of the equal ones the first `want`.  A warp owns a
+  // contiguous run of the segment: its counts, then its place in the list.
+  const int run = ((n + EVICT_THREADS - 1) / EVICT_THREADS) * 32;
+  const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
   uint32_t gt = 0, eq = 0;
-  for (int i = s0 + tid; i < s1; i += EVICT_THREADS) {
-    const uint32_t k = mass_key(__ldg(mass + i));
-    gt += k > prefix;
-    eq += k == prefix;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < r1 ? key(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < r1 && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i < r1 && k == prefix));
   }
-  uint32_t tg, te;
-  block_scan(gt, red, tg);
-  block_scan(eq, red, te);
-  if (tid == 0) {
-    cnt_s[0] = tg;
-    cnt_s[1] = te;
+  if (lane == 0) {
+    warp_s[0][warp] = gt;
+    warp_s[1][warp] = eq;
   }
-  cluster_sync();
-  uint32_t g0 = 0, e0 = 0;  // keys above / equal in the segments before this one
-  for (int r = 0; r < rank; ++r) {
-    g0 += ld_cluster(&cnt_s[0], r);
-    e0 += ld_cluster(&cnt_s[1], r);
-  }
-  for (int base = s0; base < s1; base += 4 * EVICT_THREADS) {
-    uint32_t k[4], mine = 0;  // keys above in the upper half, equal in the lower
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = base + 4 * tid + e;
-      k[e] = i < s1 ? mass_key(__ldg(mass + i)) : 0u;
-      if (i < s1) mine += (k[e] > prefix ? 0x10000u : 0u) + (k[e] == prefix ? 1u : 0u);
-    }
-    uint32_t total;
-    const uint32_t before = block_scan(mine, red, total);
-    uint32_t gb = g0 + (before >> 16), eb = e0 + (before & 0xffffu);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = base + 4 * tid + e;
-      if (i < s1) {
-        const bool above = k[e] > prefix, equal = k[e] == prefix;
-        if (above || (equal && eb < want)) kept[p.sink + gb + min(eb, want)] = p.sink + i;
-        gb += above;
-        eb += equal;
+  __syncthreads();
+  uint32_t g0 = 0, e0 = 0;  // keys above / equal before this warp's run
+  {
+    const uint32_t g = lane < EVICT_THREADS / 32 ? warp_s[0][lane] : 0u;
+    const uint32_t q = lane < EVICT_THREADS / 32 ? warp_s[1][lane] : 0u;
+    if (warp == 0) {
+      const int tg = warp_sum_int((int)g), tq = warp_sum_int((int)q);
+      if (lane == 0) {
+        cnt_s[0] = tg;
+        cnt_s[1] = tq;
       }
     }
-    g0 += total >> 16;
-    e0 += total & 0xffffu;
+    g0 = warp_sum_int(lane < warp ? (int)g : 0);
+    e0 = warp_sum_int(lane < warp ? (int)q : 0);
   }
-  cluster_sync();  // the counts above are read by the others
+  cluster_sync();
+  {  // and in the segments before this one
+    const bool other = lane < rank;
+    g0 += warp_sum_int(other ? (int)ld_cluster(&cnt_s[0], other ? lane : 0) : 0);
+    e0 += warp_sum_int(other ? (int)ld_cluster(&cnt_s[1], other ? lane : 0) : 0);
+  }
+  cluster_arrive();  // the others' counts are read; they may leave once all have come this far
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < r1 ? key(i) : 0u;
+    const bool above = i < r1 && k > prefix, equal = i < r1 && k == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+    const uint32_t eb = e0 + __popc(be & below);
+    if (above || (equal && eb < want))
+      kept[p.sink + g0 + __popc(bg & below) + min(eb, want)] = p.sink + s0 + i;
+    g0 += __popc(bg);
+    e0 += __popc(be);
+  }
+  cluster_wait();
 }
 
 constexpr int GATHER_THREADS = 256;
@@ -206,7 +268,8 @@ __global__ void __launch_bounds__(GATHER_THREADS) evict_gather_kernel(const Evic
   constexpr int LPR = D / 8;                     // lanes a row, 16 bytes each
   constexpr int RPB = GATHER_THREADS / LPR;      // rows a pass
   const int hk = blockIdx.y, b = blockIdx.z;
-  const int kv = __ldg(p.kv_len + b);  // new_len may be written over it: the same minimum
+  pdl_wait();
+  const int kv = __ldcg(p.kv_len + b);  // new_len may be written over it: the same minimum
   if (kv < 0 || kv > p.max_kv) return;
   const int n = min(kv, p.budget);
   if (blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) p.new_len[b] = n;
@@ -218,7 +281,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) evict_gather_kernel(const Evic
 #pragma unroll
   for (int e = 0; e < GATHER_UNROLL; ++e) {
     const int j = r0 + e * RPB;
-    src[e] = j < n ? __ldg(kept + j) : -1;
+    src[e] = j < n ? __ldcg(kept + j) : -1;
   }
 #pragma unroll
   for (int e = 0; e < GATHER_UNROLL; ++e) {

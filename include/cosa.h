@@ -412,7 +412,7 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * (and the window and distances below) count the kept keys, while the rotation of
  * cosa_chunk_write takes its own position values. */
 typedef struct {
-  int32_t batch;          /* B, at most 8192                                       */
+  int32_t batch;          /* B, at most 4096                                       */
   int32_t num_q_heads;    /* H_q                                                   */
   int32_t num_kv_heads;   /* H_kv, divides H_q; H_q / H_kv <= 128                  */
   int32_t head_dim;       /* D, 64 or 128                                          */
