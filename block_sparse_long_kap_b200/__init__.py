@@ -728,6 +728,15 @@ def _current_device() -> int:
     return torch.cuda.current_device()
 
 
+def _stream_on(stream, dev) -> int:
+    """The raw stream: the given one, or torch's current one on device dev (looked up by index:
+    the lookup without one costs three times as much, and a decode step is a few microseconds)."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _stream(stream)
+
+
 def cosa_chunk_write(shape: ChunkShape, rope: Optional[RopeParams], q_tok, k_tok, v_tok, positions,
                      inv_freq, cu_q, kv_len, page_table, q, k_pool, v_pool, stream=None) -> None:
     """Rotate the new tokens' Q and K (positions int32 [axes][total_q], inv_freq fp32 [pairs];
@@ -754,7 +763,7 @@ def cosa_chunk_write(shape: ChunkShape, rope: Optional[RopeParams], q_tok, k_tok
         ctypes.byref(s), None if r is None else ctypes.byref(r), _ptr(q_tok), sq, _ptr(k_tok), sk,
         _ptr(v_tok), sv, None if r is None else _ptr(positions), None if r is None else _ptr(inv_freq),
         _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(q), so, _ptr(k_pool), _ptr(v_pool),
-        _stream(stream)), "cosa_chunk_write")
+        _stream_on(stream, dev)), "cosa_chunk_write")
 
 
 def cosa_chunk_attention_workspace_size(shape: ChunkShape) -> int:
@@ -788,7 +797,7 @@ def cosa_chunk_attention(shape: ChunkShape, q, k_pool, v_pool, page_table, cu_q,
     _check(lib().cosa_chunk_attention(
         ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
         _ptr(v_pool), _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_on(stream, dev)),
         "cosa_chunk_attention")
 
 
@@ -810,7 +819,7 @@ def cosa_attention_mass(shape: ChunkShape, q, k_pool, page_table, cu_q, kv_len, 
     _check(lib().cosa_attention_mass(
         ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
         _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(lse), int(last_q), float(decay),
-        _ptr(mass), _stream(stream)), "cosa_attention_mass")
+        _ptr(mass), _stream_on(stream, dev)), "cosa_attention_mass")
 
 
 def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page_table, kv_len, mass,
@@ -834,4 +843,4 @@ def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page
     _check(lib().cosa_cache_evict(
         ctypes.byref(s), ctypes.byref(e), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
         _ptr(kv_len), _ptr(mass), _ptr(dst_table), _ptr(kept), _ptr(new_len), _ptr(mass_out),
-        _stream(stream)), "cosa_cache_evict")
+        _stream_on(stream, dev)), "cosa_cache_evict")

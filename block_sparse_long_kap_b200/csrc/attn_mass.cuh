@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(384, 1)
   struct Walk {
     long long p;
     int w, hk, b;                  // pair within the head, head, sequence
+    int from, to;                  // the sequence's pairs
     bool fresh;                    // another head or sequence than the pair before
     ChunkSeq seq;
     int tok0, ntok, pos0, prefix, ntile;  // rows: the last tokens of the chunk
@@ -170,12 +171,13 @@ __global__ void __launch_bounds__(384, 1)
     int t0, t1;                    // tiles that may see a key of the pair
   };
   auto find = [&](Walk& r) {
-    const int hk0 = r.hk, b0 = r.b;
-    while (r.w >= base) {
-      r.w -= base;
-      ++r.hk;
-    }
-    if (b0 < 0 || r.w < cum[b0] || r.w >= cum[b0 + 1]) {
+    r.fresh = false;
+    if (r.w < r.from || r.w >= r.to) {
+      r.fresh = true;
+      while (r.w >= base) {
+        r.w -= base;
+        ++r.hk;
+      }
       int lo = 0, hi = B - 1;  // the last sequence whose first pair is at or before w
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -183,6 +185,8 @@ __global__ void __launch_bounds__(384, 1)
         else hi = mid - 1;
       }
       r.b = lo;
+      r.from = cum[lo];
+      r.to = cum[lo + 1];
       r.seq = chunk_seq(prm.seqs, lo);
       const int skip = (prm.last_q > 0 && prm.last_q < r.seq.q_len) ? r.seq.q_len - prm.last_q : 0;
       r.tok0 = r.seq.q0 + skip;
@@ -191,8 +195,7 @@ __global__ void __launch_bounds__(384, 1)
       r.prefix = prm.mask.prefix_len ? __ldg(prm.mask.prefix_len + lo) : 0;
       r.ntile = (r.ntok + TOK - 1) / TOK;
     }
-    r.fresh = r.hk != hk0 || r.b != b0;
-    r.kb = 2 * (r.w - cum[r.b]);
+    r.kb = 2 * (r.w - r.from);
     r.nw = min(2, (r.seq.kv + C::KB - 1) / C::KB - r.kb);
     r.t0 = 0;
     r.t1 = r.ntile;
@@ -207,13 +210,11 @@ __global__ void __launch_bounds__(384, 1)
   Walk r;
   r.p = first;
   r.hk = 0;
-  r.b = -1;
-  r.w = 0;
+  r.w = r.from = r.to = 0;
   if (first < last) {
     r.hk = (int)(first / base);
     r.w = (int)(first - (long long)r.hk * base);
     find(r);
-    r.fresh = true;
   }
   auto next = [&]() {
     r.p += step;
@@ -405,6 +406,9 @@ __global__ void __launch_bounds__(384, 1)
       f32x2 sum[2] = {both(0.f), both(0.f)};
       Row v;
       if (!prm.held && r.t0 < r.t1) v = load_row(r.t0);
+      float* mass = prm.mass + ((long long)r.b * prm.num_kv_heads + r.hk) * prm.mass_stride + key;
+      float old = 0.f;  // fetched now, needed after the sums
+      if (key < r.seq.kv - r.seq.q_len && prm.decay != 0.f) old = *mass;
       for (int t = r.t0; t < r.t1; ++t, ++n) {
         const int sbuf = 2 * w + (n & 1);
         const MassRows* m = rows_s + t;
@@ -459,17 +463,27 @@ __global__ void __launch_bounds__(384, 1)
         };
         auto sweep = [&](auto mask_tag) {
           const uint32_t t_s = t_row + sbuf * 128;
-          uint32_t va[16], vb[16];
-          tmem_ld16_async(t_s, va);
+          int c0 = 0;
+          if (prm.cols >= 64) {
+            uint32_t va[32], vb[32];
+            tmem_ld32_async(t_s, va);
 #pragma unroll 1
-          for (int c0 = 0; c0 < prm.cols; c0 += 32) {
-            tmem_ld_wait16(va);
-            if (c0 + 16 < prm.cols) tmem_ld16_async(t_s + c0 + 16, vb);
-            add(mask_tag, va, c0);
-            if (c0 + 16 >= prm.cols) break;
-            tmem_ld_wait16(vb);
-            if (c0 + 32 < prm.cols) tmem_ld16_async(t_s + c0 + 32, va);
-            add(mask_tag, vb, c0 + 16);
+            for (; c0 + 64 <= prm.cols; c0 += 64) {
+              tmem_ld_wait32(va);
+              tmem_ld32_async(t_s + c0 + 32, vb);
+              add(mask_tag, va, c0);
+              add(mask_tag, va + 16, c0 + 16);
+              tmem_ld_wait32(vb);
+              if (c0 + 128 <= prm.cols) tmem_ld32_async(t_s + c0 + 64, va);
+              add(mask_tag, vb, c0 + 32);
+              add(mask_tag, vb + 16, c0 + 48);
+            }
+          }
+#pragma unroll 1
+          for (; c0 < prm.cols; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(t_s + c0, v);
+            add(mask_tag, v, c0);
           }
         };
         if (plain) sweep(std::false_type{});
@@ -479,12 +493,9 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(b_sfree(sbuf));
       }
       if (ok && key < r.seq.kv) {
-        float* m = prm.mass + ((long long)r.b * prm.num_kv_heads + r.hk) * prm.mass_stride + key;
-        float old = 0.f;
-        if (key < r.seq.kv - r.seq.q_len && prm.decay != 0.f) old = prm.decay * *m;
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
-        *m = old + (s0 + s1);
+        *mass = fmaf(prm.decay, old, s0 + s1);
       }
     }
   }

@@ -1,6 +1,7 @@
 // C-ABI entry points of libcosa.so: argument validation, workspace layout and
 // kernel launches.  All arithmetic of the method runs in the kernels included
 // below; this file only checks sizes and marshals pointers.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -532,6 +533,30 @@ ChunkLayout chunk_layout(const cosa_chunk_t* s) {
   return L;
 }
 
+unsigned long long current_context_id();
+
+// Opt a kernel in to `bytes` of dynamic shared memory, once per kernel, device and context (the
+// call costs about a microsecond, a decode step a few; a device reset starts a new context).
+// A kernel is always asked for the same bytes; threads that get here first at once all make
+// the call, with the same effect.
+constexpr int kAttrDevices = 64;
+template <auto Kern>
+cosa_status_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done[kAttrDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return COSA_ERR_CUDA;
+  const unsigned long long ctx = current_context_id();
+  const bool keep = dev < kAttrDevices && ctx != 0;
+  if (keep && done[dev].load(std::memory_order_acquire) == ctx) return COSA_OK;
+  if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return COSA_ERR_CUDA;
+  }
+  if (keep) done[dev].store(ctx, std::memory_order_release);
+  return COSA_OK;
+}
+
 // a launch whose prologue may overlap the end of the kernel before it
 template <typename... KArgs, typename... Args>
 cosa_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
@@ -565,12 +590,11 @@ cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
       !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size) ||
       !make_map(&mv, v_pool, D, s->page_size, PZ, s->page_size))
     return COSA_ERR_CUDA;
-  auto kern = chunk_attn_kernel<D, NT, CAP, BIAS>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Cfg::SMEM_ALLOC) != cudaSuccess)
-    return COSA_ERR_CUDA;
+  constexpr auto kern = chunk_attn_kernel<D, NT, CAP, BIAS>;
+  cosa_status_t e = allow_smem<kern>((int)Cfg::SMEM_ALLOC);
+  if (e != COSA_OK) return e;
   chunk_plan_kernel<<<1, PLAN_THREADS, (size_t)(s->batch + 1) * sizeof(int), st>>>(prm);
-  cosa_status_t e = last_launch();
+  e = last_launch();
   if (e != COSA_OK) return e;
   e = launch_pdl(kern, dim3(NUM_SMS), Cfg::THREADS, Cfg::SMEM_ALLOC, st, mq, mk, mv, prm);
   if (e != COSA_OK) return e;
@@ -599,10 +623,9 @@ cosa_status_t launch_mass_t(const cosa_chunk_t* s, const MassParams& prm, const 
   if (!make_map_q(&mq, q, s, q_stride, prm.box_tokens) ||
       !make_map(&mk, k_pool, D, s->page_size, PZ, s->page_size))
     return COSA_ERR_CUDA;
-  auto kern = attn_mass_kernel<D, CAP, BIAS>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Cfg::smem(CHUNK_MAX_BATCH)) != cudaSuccess)
-    return COSA_ERR_CUDA;
+  constexpr auto kern = attn_mass_kernel<D, CAP, BIAS>;
+  const cosa_status_t e = allow_smem<kern>((int)Cfg::smem(CHUNK_MAX_BATCH));
+  if (e != COSA_OK) return e;
   kern<<<NUM_SMS, Cfg::THREADS, Cfg::smem(s->batch), st>>>(mq, mk, prm);
   return last_launch();
 }
@@ -1402,9 +1425,8 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
   p.seg_cap = seg <= EVICT_SEG_MAX ? seg : 0;
   const size_t smem = (size_t)p.seg_cap * sizeof(uint32_t);
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           EVICT_SEG_MAX * (int)sizeof(uint32_t)) != cudaSuccess)
-    return COSA_ERR_CUDA;
+  e = allow_smem<evict_select_kernel>(EVICT_SEG_MAX * (int)sizeof(uint32_t));
+  if (e != COSA_OK) return e;
   evict_select_kernel<<<dim3(EVICT_CL, shape->num_kv_heads, shape->batch), EVICT_THREADS, smem,
                         st>>>(p);
   e = last_launch();
