@@ -810,22 +810,38 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
   if (r >= p.tile_tokens * G || tok >= jn.x) return;
   const int c0 = blockIdx.x, n = last - c0 + 1;
   auto slot = [&](int s) { return (long long)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.part_rows + row; };
-  float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldcg(p.part_ml + slot(s)).x);
-  m = warp_max(m);
-  float l = 0.f, o[EPL];
+  float l = 0.f, m = -INFINITY, o[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  if (m != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const long long at = slot(s);
-      const float2 ml = __ldcg(p.part_ml + at);
-      const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - m) : 0.f;
-      l = fmaf(w, ml.y, l);
-      const float* src = p.part_o + at * D + lane * EPL;
+  // 32 parts at a time: a lane holds one part's base and sum, the rows come eight loads deep
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int cnt = min(32, n - s0);
+    const float2 ml = lane < cnt ? __ldcg(p.part_ml + slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
+    const float mx = fmaxf(m, warp_max(ml.x));
+    if (mx == -INFINITY) continue;
+    const float back = tc::ex2_approx(m - mx);  // (from -inf: 0)
+    const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - mx) : 0.f;
+    float part = w * ml.y;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, __ldcg(src + e), o[e]);
+    for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+    l = fmaf(l, back, part);
+    m = mx;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= back;
+#pragma unroll 8
+    for (int s = 0; s < cnt; ++s) {
+      const float* src = p.part_o + slot(s0 + s) * D + lane * EPL;
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      float v[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; e += 2) {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(src + e));
+        v[e] = t.x;
+        v[e + 1] = t.y;
+      }
+      // (a part without keys has no weight, whatever its O holds)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = ws > 0.f ? fmaf(ws, v[e], o[e]) : o[e];
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -19,6 +19,7 @@
 #include "decode.cuh"
 #include "chunk_write.cuh"
 #include "chunk_attn.cuh"
+#include "chunk_decode.cuh"
 #include "attn_mass.cuh"
 #include "evict.cuh"
 
@@ -579,6 +580,13 @@ cosa_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
   return COSA_OK;
 }
 
+template <int D>
+cosa_status_t launch_join(const ChunkAttnParams& prm, cudaStream_t st) {
+  return launch_pdl(chunk_combine_kernel<D>,
+                    dim3(NUM_SMS, (prm.part_rows + JOIN_WARPS - 1) / JOIN_WARPS), 32 * JOIN_WARPS,
+                    0, st, prm);
+}
+
 template <int D, int NT, bool CAP, bool BIAS>
 cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, const void* q,
                              int64_t q_stride, const void* k_pool, const void* v_pool,
@@ -598,9 +606,37 @@ cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
   if (e != COSA_OK) return e;
   e = launch_pdl(kern, dim3(NUM_SMS), Cfg::THREADS, Cfg::SMEM_ALLOC, st, mq, mk, mv, prm);
   if (e != COSA_OK) return e;
-  return launch_pdl(chunk_combine_kernel<D>,
-                    dim3(NUM_SMS, (prm.part_rows + JOIN_WARPS - 1) / JOIN_WARPS), 32 * JOIN_WARPS,
-                    0, st, prm);
+  return launch_join<D>(prm, st);
+}
+
+template <int N, bool CAP, bool BIAS>
+cosa_status_t launch_decode_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm,
+                                    const void* q, int64_t q_stride, const void* k_pool,
+                                    const void* v_pool, cudaStream_t st) {
+  using Cfg = DecCfg<N>;
+  CUtensorMap mq, mk, mv;
+  const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
+  if (!make_map_q(&mq, q, s, q_stride, s->max_q) ||
+      !make_map(&mk, k_pool, 128, s->page_size, PZ, s->page_size) ||
+      !make_map(&mv, v_pool, 128, s->page_size, PZ, s->page_size))
+    return COSA_ERR_CUDA;
+  constexpr auto kern = chunk_decode_kernel<N, CAP, BIAS>;
+  cosa_status_t e = allow_smem<kern>((int)Cfg::SMEM);
+  if (e != COSA_OK) return e;
+  kern<<<NUM_SMS, Cfg::THREADS, Cfg::SMEM, st>>>(mq, mk, mv, prm);
+  e = last_launch();
+  return e != COSA_OK ? e : launch_join<128>(prm, st);
+}
+
+template <int N>
+cosa_status_t launch_decode_chunk(const cosa_chunk_t* s, const ChunkAttnParams& prm, bool cap,
+                                  const void* q, int64_t q_stride, const void* k_pool,
+                                  const void* v_pool, cudaStream_t st) {
+  const bool bias = prm.slopes != nullptr;
+  if (cap && bias) return launch_decode_chunk_t<N, true, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (cap) return launch_decode_chunk_t<N, true, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (bias) return launch_decode_chunk_t<N, false, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  return launch_decode_chunk_t<N, false, false>(s, prm, q, q_stride, k_pool, v_pool, st);
 }
 
 template <int D, int NT>
@@ -1334,6 +1370,12 @@ cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_p
   p.timeout_ns = kWaitTimeoutNs;
   const bool cap = score && score->softcap > 0.f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // A few rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
+  // 32K keys (7 rows): DECODE_NEW against DECODE_OLD us for the 128-row form.
+  const int rows = shape->max_q * p.group;
+  if (shape->head_dim == 128 && rows <= 32)
+    return rows <= 16 ? launch_decode_chunk<16>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
+                      : launch_decode_chunk<32>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
   if (shape->head_dim == 128)
     return L.nt == 1 ? launch_chunk_n<128, 1>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
                      : launch_chunk_n<128, 2>(shape, p, cap, q, q_stride, k_pool, v_pool, st);

@@ -98,8 +98,13 @@ class Case:
         lse = torch.full((self.T, self.hq), 7.0, device="cuda")
         if ws is None:
             ws = torch.full((C.cosa_chunk_attention_workspace_size(self.shape),), 255, dtype=torch.uint8, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())  # the buffers were filled there
         C.cosa_chunk_attention(self.shape, d["q"] if q is None else q, d["k_pool"], d["v_pool"], d["table"], d["cu"],
                                d["kv"], out, ws, score=score, lse=lse, stream=stream)
+        if stream is not None:  # and are not handed out again before this stream is done with them
+            for t in (out, lse, ws):
+                t.record_stream(stream)
         return out, lse
 
     def oracle(self, kw):
