@@ -794,6 +794,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 
 // ---- join of the tiles that were cut ----------------------------------------------------
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_DEEP = 16;  // loads of a row in flight: the join is all latency
 
 // grid (NUM_SMS, row groups); one row a warp
 template <int D>
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
   float l = 0.f, m = -INFINITY, o[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  // 32 parts at a time: a lane holds one part's base and sum, the rows come eight loads deep
+  // 32 parts at a time: a lane holds one part's base and sum, the rows come many loads deep
   for (int s0 = 0; s0 < n; s0 += 32) {
     const int cnt = min(32, n - s0);
     const float2 ml = lane < cnt ? __ldcg(p.part_ml + slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
@@ -828,20 +829,26 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
     m = mx;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) o[e] *= back;
-#pragma unroll 8
-    for (int s = 0; s < cnt; ++s) {
-      const float* src = p.part_o + slot(s0 + s) * D + lane * EPL;
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      float v[EPL];
+    for (int s = 0; s < cnt; s += JOIN_DEEP) {
+      float v[JOIN_DEEP][EPL];
 #pragma unroll
-      for (int e = 0; e < EPL; e += 2) {
-        const float2 t = __ldcg(reinterpret_cast<const float2*>(src + e));
-        v[e] = t.x;
-        v[e + 1] = t.y;
+      for (int x = 0; x < JOIN_DEEP; ++x) {
+        const float* src = p.part_o + slot(s0 + min(s + x, cnt - 1)) * D + lane * EPL;
+        if (EPL == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+          v[x][0] = t.x, v[x][1] = t.y, v[x][EPL - 2] = t.z, v[x][EPL - 1] = t.w;
+        } else {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+          v[x][0] = t.x, v[x][1] = t.y;
+        }
       }
-      // (a part without keys has no weight, whatever its O holds)
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = ws > 0.f ? fmaf(ws, v[e], o[e]) : o[e];
+      for (int x = 0; x < JOIN_DEEP; ++x) {
+        const float ws = __shfl_sync(0xffffffffu, w, min(s + x, 31));
+        if (s + x < cnt && ws > 0.f)  // (a part without keys has no weight, whatever its O holds)
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) o[e] = fmaf(ws, v[x][e], o[e]);
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -127,13 +127,15 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t b_ofull = bar + 8u * (B0 + 5), b_pv = bar + 8u * (B0 + 6), b_done = bar + 8u * (B0 + 7);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sg + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 4);
-  volatile int* start_s = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 8);  // sequence, offset
+  int* start_off = reinterpret_cast<int*>(sg + C::OFF_MISC + 8);
+  ChunkTile* start_s = reinterpret_cast<ChunkTile*>(sg + C::OFF_MISC + 16);
   long long* scan_s = reinterpret_cast<long long*>(sg + C::OFF_ROWS);  // (before the rows)
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = prm.group, P = prm.page_size, B = prm.seqs.batch;
-  if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) return;
+  // (an earlier launch that timed out: looked at with the plan's loads under way)
+  const bool stop = *(volatile int*)&g_status == COSA_ERR_TIMEOUT;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) { mbar_init(b_qfull(i), 1); mbar_init(b_qempty(i), 1); }
@@ -157,8 +159,14 @@ __global__ void __launch_bounds__(256, 1)
   // ---- plan: blocks of all sequences, a contiguous group of them per thread
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int bs0 = min(tid * per, B), bs1 = min(bs0 + per, B);
+  ChunkTile first;  // the group's first sequence, kept (the only one for up to 256)
+  first.nb = 0;
   long long mine = 0;
-  for (int b = bs0; b < bs1; ++b) mine += decode_tile(prm, b).nb;
+  for (int b = bs0; b < bs1; ++b) {
+    const ChunkTile d = decode_tile(prm, b);
+    if (b == bs0) first = d;
+    mine += d.nb;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -166,27 +174,33 @@ __global__ void __launch_bounds__(256, 1)
     if (lane >= o) inc += y;
   }
   if (lane == 31) scan_s[warp] = inc;
-  __syncthreads();
+  const bool stopped = __syncthreads_or(stop);
   long long before = inc - mine, per_head = 0;
+#pragma unroll
   for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) before += scan_s[w];
-    per_head += scan_s[w];
+    const long long v = scan_s[w];
+    if (w < warp) before += v;
+    per_head += v;
   }
-  const long long total = per_head * prm.num_kv_heads;
-  const long long quota = (total + gridDim.x - 1) / gridDim.x;
+  // (32-bit divisions where they do: a 64-bit one takes a tenth of a microsecond)
+  auto divide = [](long long a, long long d) -> long long {
+    return a <= 0xffffffffll && d <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)d) : a / d;
+  };
+  const long long total = stopped ? 0 : per_head * prm.num_kv_heads;
+  const long long quota = divide(total + gridDim.x - 1, gridDim.x);
   const long long w0 = min((long long)blockIdx.x * quota, total), w1 = min(w0 + quota, total);
-  const int hk0 = w0 < w1 ? (int)(w0 / per_head) : 0;
+  const int hk0 = w0 < w1 ? (int)divide(w0, per_head) : 0;
   if (w0 < w1) {
     long long rem = w0 - hk0 * per_head - before;
     if (rem >= 0 && rem < mine)
       for (int b = bs0; b < bs1; ++b) {
-        const int nb = decode_tile(prm, b).nb;
-        if (rem < nb) {
-          start_s[0] = b;
-          start_s[1] = (int)rem;
+        const ChunkTile d = b == bs0 ? first : decode_tile(prm, b);
+        if (rem < d.nb) {
+          *start_s = d;
+          *start_off = (int)rem;
           break;
         }
-        rem -= nb;
+        rem -= d.nb;
       }
   }
   __syncthreads();
@@ -199,17 +213,23 @@ __global__ void __launch_bounds__(256, 1)
     int b, hk, off;
     ChunkTile tile;
     int jb, nb, part;
+    bool have;  // tile is that of b
   } wk;
   wk.left = w1 - w0;
   wk.hk = hk0;
-  wk.b = wk.left > 0 ? start_s[0] : 0;
-  wk.off = wk.left > 0 ? start_s[1] : 0;
+  wk.b = wk.off = 0;
+  wk.have = wk.left > 0;
+  if (wk.have) {
+    wk.tile = *start_s;
+    wk.b = wk.tile.b;
+    wk.off = *start_off;
+  }
   auto next = [&]() -> bool {
     if (wk.left <= 0) return false;
-    for (;;) {  // sequences without tokens have no blocks
+    while (!wk.have) {  // sequences without tokens have no blocks
       wk.tile = decode_tile(prm, wk.b);
-      if (wk.tile.nb > 0) break;
-      if (++wk.b == B) {
+      wk.have = wk.tile.nb > 0;
+      if (!wk.have && ++wk.b == B) {
         wk.b = 0;
         ++wk.hk;
       }
@@ -223,6 +243,7 @@ __global__ void __launch_bounds__(256, 1)
   auto advance = [&]() {
     wk.left -= wk.nb;
     wk.off = 0;
+    wk.have = false;
     if (++wk.b == B) {
       wk.b = 0;
       ++wk.hk;
@@ -459,7 +480,8 @@ __global__ void __launch_bounds__(256, 1)
           const bool plain = alo <= key0 && ahi >= key0 + C::KB - 1;
 #pragma unroll
           for (int r0 = 0; r0 < N; r0 += 4) {
-            if (r0 < nrow) {
+            if (r0 >= nrow) break;  // one jump past all the code of rows that do not exist
+            {
 #pragma unroll
               for (int r = r0; r < r0 + 4; ++r) {
                 x[r] = score_log2<CAP>(prm.score, __uint_as_float(sc[r]));
@@ -475,20 +497,27 @@ __global__ void __launch_bounds__(256, 1)
           if (ok) {
             float v = 0.f;
 #pragma unroll
-            for (int r = 0; r < N; ++r)
-              if (r < nrow && lane == r) v = wmax[r];
+            for (int r0 = 0; r0 < N; r0 += 4) {
+              if (r0 >= nrow) break;
+#pragma unroll
+              for (int r = r0; r < r0 + 4; ++r)
+                if (lane == r) v = wmax[r];
+            }
             if (lane < nrow) exch[lane * 4 + q4] = v;
           }
           named_bar_sync(1, 128);
           if (ok) {
             float alpha[N];
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
-              alpha[r] = 1.f;
-              if (r < nrow) {
+            for (int r = 0; r < N; ++r) alpha[r] = 1.f;
+#pragma unroll
+            for (int r0 = 0; r0 < N; r0 += 4) {
+              if (r0 >= nrow) break;
+#pragma unroll
+              for (int r = r0; r < r0 + 4; ++r) {
                 const float4 e4 = *reinterpret_cast<const float4*>(exch + r * 4);
                 const float m = fmaxf(fmaxf(e4.x, e4.y), fmaxf(e4.z, e4.w));
-                if (m > m_ref[r] + C::kRescale) {
+                if (r < nrow && m > m_ref[r] + C::kRescale) {
                   alpha[r] = ex2_approx(m_ref[r] - m);
                   m_ref[r] = m;
                   l[r] *= alpha[r];
@@ -515,7 +544,8 @@ __global__ void __launch_bounds__(256, 1)
         if (ok) {
 #pragma unroll
           for (int r0 = 0; r0 < N; r0 += 4) {
-            if (r0 < nrow) {
+            if (r0 >= nrow) break;
+            {
 #pragma unroll
               for (int r = r0; r < r0 + 4; ++r) {
                 const float p = ex2_approx(x[r] - (m_ref[r] == -INFINITY ? 0.f : m_ref[r]));
@@ -535,11 +565,17 @@ __global__ void __launch_bounds__(256, 1)
       if (ok && !wait_warp(b_ofull, nseg & 1)) ok = false;
       ++nseg;
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        if (r < nrow) {
+      for (int r0 = 0; r0 < N; r0 += 4) {
+        if (r0 >= nrow) break;
+        {
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-          if (lane == 0) exch[r * 4 + q4] = l[r];
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+          // one 16-byte column of the sums a warp
+          if (lane < 4)
+            exch[(r0 + lane) * 4 + q4] = lane < 2 ? (lane ? l[r0 + 1] : l[r0])
+                                                  : (lane == 2 ? l[r0 + 2] : l[r0 + 3]);
         }
       }
       named_bar_sync(1, 128);
@@ -549,14 +585,14 @@ __global__ void __launch_bounds__(256, 1)
         if (N == 16) tmem_ld16(t_row + 64, o);
         else tmem_ld32(t_row + 64, o);
         const long long slot = (2 * blockIdx.x + (wk.part > 0 ? 1 : 0)) * (long long)prm.part_rows;
+        long long at = (long long)wk.tile.tok0 * prm.num_q_heads + wk.hk * G;  // row 0's
+        int g = 0;
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-          if (r < nrow) {
+          if (r >= nrow) break;
+          {
             const float4 e4 = *reinterpret_cast<const float4*>(exch + r * 4);
             const float sum = (e4.x + e4.y) + (e4.z + e4.w);
-            const int tok = r / G;
-            const long long at =
-                (long long)(wk.tile.tok0 + tok) * prm.num_q_heads + wk.hk * G + (r - tok * G);
             if (wk.part < 0) {
               const float inv = sum > 0.f ? 1.f / sum : 0.f;
               prm.out[at * D + row] = __float2bfloat16_rn(__uint_as_float(o[r]) * inv);
@@ -565,6 +601,11 @@ __global__ void __launch_bounds__(256, 1)
             } else {
               prm.part_o[(slot + r) * D + row] = __uint_as_float(o[r]);
               if (row == r) prm.part_ml[slot + r] = make_float2(m_ref[r], sum);
+            }
+            ++at;  // the next head of the group, or the next token's first
+            if (++g == G) {
+              g = 0;
+              at += prm.num_q_heads - G;
             }
           }
         }
