@@ -164,7 +164,31 @@ class ChunkShape:
     num_phys_pages: int = 0     # 0 -> batch * pages_per_seq
     softmax_scale: float = 0.0  # 0 -> 1/sqrt(head_dim)
 
+    def __setattr__(self, name, value):
+        # what c() and dims() made of the fields goes with the first change to one of them
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_c", None)
+        self.__dict__.pop("_dims", None)
+
     def c(self) -> _Chunk:
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = self.__dict__["_c"] = self._make()
+        return c
+
+    def dims(self) -> tuple:
+        """Expected shapes: q rows, k rows, lse, pool, page table, cu_q, kv_len, mass."""
+        d = self.__dict__.get("_dims")
+        if d is None:
+            s = self.c()
+            d = self.__dict__["_dims"] = (
+                (s.total_q, s.num_q_heads, s.head_dim), (s.total_q, s.num_kv_heads, s.head_dim),
+                (s.total_q, s.num_q_heads), (s.num_phys_pages, s.num_kv_heads, s.page_size, s.head_dim),
+                (s.batch, s.pages_per_seq), (s.batch + 1,), (s.batch,),
+                (s.batch, s.num_kv_heads, s.pages_per_seq * s.page_size))
+        return d
+
+    def _make(self) -> _Chunk:
         pps = self.pages_per_seq or -(-self.max_kv // max(self.page_size, 1))
         nphys = self.num_phys_pages or self.batch * pps
         scale = self.softmax_scale or 1.0 / math.sqrt(max(self.head_dim, 1))
@@ -198,14 +222,14 @@ class ScoreParams:
 
     def c(self, s: _Chunk, dev: int) -> _Score:
         import torch
+        slopes = first = prefix = None
         if self.slopes is not None:
-            _arg(self.slopes, "slopes", torch.float32, (s.num_q_heads,), dev)
+            slopes = _arg(self.slopes, "slopes", torch.float32, (s.num_q_heads,), dev)
         if self.first_key is not None:
-            _arg(self.first_key, "first_key", torch.int32, (s.total_q,), dev)
+            first = _arg(self.first_key, "first_key", torch.int32, (s.total_q,), dev)
         if self.prefix_len is not None:
-            _arg(self.prefix_len, "prefix_len", torch.int32, (s.batch,), dev)
-        return _Score(self.softcap, self.window, _ptr(self.slopes), _ptr(self.first_key),
-                      _ptr(self.prefix_len))
+            prefix = _arg(self.prefix_len, "prefix_len", torch.int32, (s.batch,), dev)
+        return _Score(self.softcap, self.window, slopes, first, prefix)
 
 
 @dataclasses.dataclass
@@ -681,8 +705,8 @@ def cosa_get_status(stream=None) -> int:
     return lib().cosa_get_status(_stream(stream))
 
 
-def _arg(t, name, dtype, shape, dev):
-    """A dense tensor on the current device."""
+def _arg(t, name, dtype, shape, dev) -> int:
+    """The address of a dense tensor on the current device."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype is not dtype:
@@ -693,34 +717,25 @@ def _arg(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+    return t.data_ptr()
 
 
-def _rows(t, name, shape, dev) -> int:
-    """A token-major bf16 tensor whose rows may be strided (a view of a fused projection);
-    returns the row stride in elements."""
-    import torch
+def _rows(t, name, dtype, shape, dev) -> tuple:
+    """Address and row stride (elements) of a token-major tensor whose rows may be strided, as
+    the views of a fused projection are."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, h, d = shape
     st = t.stride()
-    if (st[2] != 1) or (h > 1 and st[1] != d):
+    if st[2] != 1 or (h > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
-    return st[0] if n > 1 else h * d
-
-
-def _chunk_cache(s: _Chunk, k_pool, v_pool, page_table, dev) -> None:
-    import torch
-    pool = (s.num_phys_pages, s.num_kv_heads, s.page_size, s.head_dim)
-    _arg(k_pool, "k_pool", torch.bfloat16, pool, dev)
-    if v_pool is not None:
-        _arg(v_pool, "v_pool", torch.bfloat16, pool, dev)
-    _arg(page_table, "page_table", torch.int32, (s.batch, s.pages_per_seq), dev)
+    return t.data_ptr(), (st[0] if n > 1 else h * d)
 
 
 def _current_device() -> int:
@@ -744,26 +759,26 @@ def cosa_chunk_write(shape: ChunkShape, rope: Optional[RopeParams], q_tok, k_tok
     sequence's keys in the paged cache.  q_tok [total_q][H_q][D], k_tok / v_tok
     [total_q][H_kv][D] may be views of a fused projection; q may be q_tok."""
     import torch
+    bf, i32 = torch.bfloat16, torch.int32
     s, dev = shape.c(), _current_device()
-    r = None
+    dq, dk, _, dpool, dtab, dcu, dkv, _ = shape.dims()
+    r = pos = freq = None
     if rope is not None and len(rope.sections):
-        r = rope.c()
-        _arg(positions, "positions", torch.int32, (r.axes, s.total_q), dev)
-        _arg(inv_freq, "inv_freq", torch.float32, (sum(rope.sections),), dev)
-    hq, hk = (s.total_q, s.num_q_heads, s.head_dim), (s.total_q, s.num_kv_heads, s.head_dim)
-    sq, sk, sv = (_rows(q_tok, "q_tok", hq, dev), _rows(k_tok, "k_tok", hk, dev),
-                  _rows(v_tok, "v_tok", hk, dev))
-    so = _rows(q, "q", hq, dev)
-    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
-    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
-    if v_pool is None:
-        raise ValueError("v_pool is required")
-    _chunk_cache(s, k_pool, v_pool, page_table, dev)
-    _check(lib().cosa_chunk_write(
-        ctypes.byref(s), None if r is None else ctypes.byref(r), _ptr(q_tok), sq, _ptr(k_tok), sk,
-        _ptr(v_tok), sv, None if r is None else _ptr(positions), None if r is None else _ptr(inv_freq),
-        _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(q), so, _ptr(k_pool), _ptr(v_pool),
-        _stream_on(stream, dev)), "cosa_chunk_write")
+        rc = rope.c()
+        r = ctypes.byref(rc)
+        pos = _arg(positions, "positions", i32, (rc.axes, s.total_q), dev)
+        freq = _arg(inv_freq, "inv_freq", torch.float32, (sum(rope.sections),), dev)
+    pq, sq = _rows(q_tok, "q_tok", bf, dq, dev)
+    pk, sk = _rows(k_tok, "k_tok", bf, dk, dev)
+    pv, sv = _rows(v_tok, "v_tok", bf, dk, dev)
+    po, so = _rows(q, "q", bf, dq, dev)
+    st = lib().cosa_chunk_write(
+        ctypes.byref(s), r, pq, sq, pk, sk, pv, sv, pos, freq, _arg(cu_q, "cu_q", i32, dcu, dev),
+        _arg(kv_len, "kv_len", i32, dkv, dev), _arg(page_table, "page_table", i32, dtab, dev), po, so,
+        _arg(k_pool, "k_pool", bf, dpool, dev), _arg(v_pool, "v_pool", bf, dpool, dev),
+        _stream_on(stream, dev))
+    if st:
+        raise CosaError(st, "cosa_chunk_write")
 
 
 def cosa_chunk_attention_workspace_size(shape: ChunkShape) -> int:
@@ -780,25 +795,22 @@ def cosa_chunk_attention(shape: ChunkShape, q, k_pool, v_pool, page_table, cu_q,
     """Exact attention of every sequence's new tokens (q [total_q][H_q][D]) over its cache,
     with the score shaped and masked by `score` (None: plain causal)."""
     import torch
+    bf, i32 = torch.bfloat16, torch.int32
     s, dev = shape.c(), _current_device()
-    hq = (s.total_q, s.num_q_heads, s.head_dim)
-    sq = _rows(q, "q", hq, dev)
-    if v_pool is None:
-        raise ValueError("v_pool is required")
-    _chunk_cache(s, k_pool, v_pool, page_table, dev)
-    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
-    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
-    _arg(out, "out", torch.bfloat16, hq, dev)
-    if lse is not None:
-        _arg(lse, "lse", torch.float32, hq[:2], dev)
+    dq, _, dlse, dpool, dtab, dcu, dkv, _ = shape.dims()
+    pq, sq = _rows(q, "q", bf, dq, dev)
+    pk, pv = _arg(k_pool, "k_pool", bf, dpool, dev), _arg(v_pool, "v_pool", bf, dpool, dev)
+    tab, cu = _arg(page_table, "page_table", i32, dtab, dev), _arg(cu_q, "cu_q", i32, dcu, dev)
+    kv = _arg(kv_len, "kv_len", i32, dkv, dev)
+    po = _arg(out, "out", bf, dq, dev)
+    pl = None if lse is None else _arg(lse, "lse", torch.float32, dlse, dev)
     if workspace is None or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
-    sc = None if score is None else score.c(s, dev)
-    _check(lib().cosa_chunk_attention(
-        ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
-        _ptr(v_pool), _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_on(stream, dev)),
-        "cosa_chunk_attention")
+    st = lib().cosa_chunk_attention(
+        ctypes.byref(s), None if score is None else ctypes.byref(score.c(s, dev)), pq, sq, pk, pv, tab,
+        cu, kv, po, pl, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        raise CosaError(st, "cosa_chunk_attention")
 
 
 def cosa_attention_mass(shape: ChunkShape, q, k_pool, page_table, cu_q, kv_len, lse, mass,
@@ -808,18 +820,18 @@ def cosa_attention_mass(shape: ChunkShape, q, k_pool, page_table, cu_q, kv_len, 
     ([B][H_kv][pages_per_seq * P], in place): those of each sequence's last last_q new tokens
     (0: all), summed over the heads of the group; old masses are first multiplied by decay."""
     import torch
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     s, dev = shape.c(), _current_device()
-    sq = _rows(q, "q", (s.total_q, s.num_q_heads, s.head_dim), dev)
-    _chunk_cache(s, k_pool, None, page_table, dev)
-    _arg(cu_q, "cu_q", torch.int32, (s.batch + 1,), dev)
-    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
-    _arg(lse, "lse", torch.float32, (s.total_q, s.num_q_heads), dev)
-    _arg(mass, "mass", torch.float32, (s.batch, s.num_kv_heads, s.pages_per_seq * s.page_size), dev)
-    sc = None if score is None else score.c(s, dev)
-    _check(lib().cosa_attention_mass(
-        ctypes.byref(s), None if sc is None else ctypes.byref(sc), _ptr(q), sq, _ptr(k_pool),
-        _ptr(page_table), _ptr(cu_q), _ptr(kv_len), _ptr(lse), int(last_q), float(decay),
-        _ptr(mass), _stream_on(stream, dev)), "cosa_attention_mass")
+    dq, _, dlse, dpool, dtab, dcu, dkv, dmass = shape.dims()
+    pq, sq = _rows(q, "q", bf, dq, dev)
+    pk, tab = _arg(k_pool, "k_pool", bf, dpool, dev), _arg(page_table, "page_table", i32, dtab, dev)
+    cu, kv = _arg(cu_q, "cu_q", i32, dcu, dev), _arg(kv_len, "kv_len", i32, dkv, dev)
+    pl, pm = _arg(lse, "lse", f32, dlse, dev), _arg(mass, "mass", f32, dmass, dev)
+    st = lib().cosa_attention_mass(
+        ctypes.byref(s), None if score is None else ctypes.byref(score.c(s, dev)), pq, sq, pk, tab, cu,
+        kv, pl, last_q, decay, pm, _stream_on(stream, dev))
+    if st:
+        raise CosaError(st, "cosa_attention_mass")
 
 
 def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page_table, kv_len, mass,
@@ -828,19 +840,17 @@ def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page
     others): their positions to kept [B][H_kv][budget] (ascending, -1 past the end), their K, V
     and mass to the pages of dst_table [B][ceil(budget / P)], the new lengths to new_len."""
     import torch
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     s, e, dev = shape.c(), evict.c(), _current_device()
-    if v_pool is None:
-        raise ValueError("v_pool is required")
-    _chunk_cache(s, k_pool, v_pool, page_table, dev)
-    pages = -(-e.budget // s.page_size)
-    _arg(kv_len, "kv_len", torch.int32, (s.batch,), dev)
-    _arg(mass, "mass", torch.float32, (s.batch, s.num_kv_heads, s.pages_per_seq * s.page_size), dev)
-    _arg(dst_table, "dst_table", torch.int32, (s.batch, pages), dev)
-    _arg(kept, "kept", torch.int32, (s.batch, s.num_kv_heads, e.budget), dev)
-    _arg(new_len, "new_len", torch.int32, (s.batch,), dev)
-    if mass_out is not None:
-        _arg(mass_out, "mass_out", torch.float32, (s.batch, s.num_kv_heads, pages * s.page_size), dev)
-    _check(lib().cosa_cache_evict(
-        ctypes.byref(s), ctypes.byref(e), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
-        _ptr(kv_len), _ptr(mass), _ptr(dst_table), _ptr(kept), _ptr(new_len), _ptr(mass_out),
-        _stream_on(stream, dev)), "cosa_cache_evict")
+    _, _, _, dpool, dtab, _, dkv, dmass = shape.dims()
+    n, hk, pages = s.batch, s.num_kv_heads, -(-e.budget // s.page_size)
+    st = lib().cosa_cache_evict(
+        ctypes.byref(s), ctypes.byref(e), _arg(k_pool, "k_pool", bf, dpool, dev),
+        _arg(v_pool, "v_pool", bf, dpool, dev), _arg(page_table, "page_table", i32, dtab, dev),
+        _arg(kv_len, "kv_len", i32, dkv, dev), _arg(mass, "mass", f32, dmass, dev),
+        _arg(dst_table, "dst_table", i32, (n, pages), dev),
+        _arg(kept, "kept", i32, (n, hk, e.budget), dev), _arg(new_len, "new_len", i32, dkv, dev),
+        None if mass_out is None else _arg(mass_out, "mass_out", f32, (n, hk, pages * s.page_size), dev),
+        _stream_on(stream, dev))
+    if st:
+        raise CosaError(st, "cosa_cache_evict")
