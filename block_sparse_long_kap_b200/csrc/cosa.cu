@@ -1301,7 +1301,7 @@ cosa_status_t cosa_chunk_write(const cosa_chunk_t* shape, const cosa_rope_params
   // tokens share a CTA's setup while four CTAs an SM are left; a few tokens are split by
   // heads instead, one unit a thread
   long long tpb = shape->total_q / (4 * NUM_SMS);
-  p.tokens_per_cta = tpb < 1 ? 1 : (tpb > 8 ? 8 : (int)tpb);
+  p.tokens_per_cta = tpb < 1 ? 1 : (tpb > 4 ? 4 : (int)tpb);
   const int blocks = (shape->total_q + p.tokens_per_cta - 1) / p.tokens_per_cta;
   p.units_per_part = (int)units;
   if (blocks < 2 * NUM_SMS && units > CHUNK_WRITE_THREADS)
