@@ -190,16 +190,21 @@ struct ChunkCfg {
   static constexpr uint32_t OFF_K = OFF_Q + NT * Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + KS * BLK_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_V + VS * BLK_BYTES;
-  // q full / empty, k full / empty, v full / empty, v tail, s full[2],
-  // p full[2][half], o full[2], pv done, done
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 8 + 2;
+  // q full / empty, k full / empty, v full / empty, v tail, s full[2][2], p full[2][2],
+  // o full[2], pv done[2], done[2]
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 8 + 4 + 2;
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBAR * 8 + 15) & ~15u;
   static constexpr uint32_t SMEM = OFF_MISC + 32;   // TMEM address, abort, start tile
   static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
-  static constexpr int COL_O = 256;                 // S buffers at 0 and 128
+  static constexpr int COL_O = 256;                 // S buffers: tile i at 128 i, 64 columns each
   static constexpr float kRescale = 8.0f;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 };
+
+// Half blocks of 64 keys that nb blocks from one with `keys` keys left on hold.
+__device__ __forceinline__ int half_blocks(int nb, int keys) {
+  return min(2 * nb, max((keys + 63) >> 6, 1));
+}
 
 // A CTA's walk over its share [w, w_end) of the plan; every role walks by itself.
 struct ChunkWalk {
@@ -252,10 +257,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   auto b_vempty = [&](int s) { return bar + 8u * (2 + 2 * C::KS + C::VS + s); };
   constexpr int B0 = 2 + 2 * C::KS + 2 * C::VS;
   const uint32_t b_vtail = bar + 8u * B0;
-  auto b_sfull = [&](int i) { return bar + 8u * (B0 + 1 + i); };
-  auto b_pfull = [&](int i, int h) { return bar + 8u * (B0 + 3 + 2 * i + h); };
-  auto b_ofull = [&](int i) { return bar + 8u * (B0 + 7 + i); };
-  const uint32_t b_pv = bar + 8u * (B0 + 9), b_done = bar + 8u * (B0 + 10);
+  auto b_sfull = [&](int i, int buf) { return bar + 8u * (B0 + 1 + 2 * i + buf); };
+  auto b_pfull = [&](int i, int buf) { return bar + 8u * (B0 + 5 + 2 * i + buf); };
+  auto b_ofull = [&](int i) { return bar + 8u * (B0 + 9 + i); };
+  auto b_pv = [&](int i) { return bar + 8u * (B0 + 11 + i); };
+  auto b_done = [&](int i) { return bar + 8u * (B0 + 13 + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sg + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 4);
   volatile int* start_tile = reinterpret_cast<volatile int*>(sg + C::OFF_MISC + 8);
@@ -267,18 +273,21 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 
   if (tid == 0) {
     mbar_init(b_qfull, 1);
-    mbar_init(b_qempty, 1);
-    for (int s = 0; s < C::KS; ++s) { mbar_init(b_kfull(s), 1); mbar_init(b_kempty(s), 1); }
-    for (int s = 0; s < C::VS; ++s) { mbar_init(b_vfull(s), 1); mbar_init(b_vempty(s), 1); }
+    // a slot is free when the issuers of both tiles have let it go
+    mbar_init(b_qempty, NT);
+    for (int s = 0; s < C::KS; ++s) { mbar_init(b_kfull(s), 1); mbar_init(b_kempty(s), NT); }
+    for (int s = 0; s < C::VS; ++s) { mbar_init(b_vfull(s), 1); mbar_init(b_vempty(s), NT); }
     mbar_init(b_vtail, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(b_sfull(i), 1);
-      mbar_init(b_pfull(i, 0), 4);
-      mbar_init(b_pfull(i, 1), 4);
+      for (int buf = 0; buf < 2; ++buf) {
+        mbar_init(b_sfull(i, buf), 1);
+        mbar_init(b_pfull(i, buf), 4);
+      }
       mbar_init(b_ofull(i), 1);
+      mbar_init(b_pv(i), 1);
     }
-    mbar_init(b_pv, 1);
-    mbar_init(b_done, 1);
+    mbar_init(b_done(0), 1);
+    mbar_init(b_done(1), 1);
     *abort_flag = 0;
     *start_tile = 0;
     fence_barrier_init();
@@ -455,97 +464,86 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         drain_wait(b_vfull(x % C::VS), (x / C::VS) & 1, t0, tmo);
       if (tails > 0) drain_wait(b_vtail, (tails - 1) & 1, t0, tmo);
     }
-  } else if (warp == 1) {
-    // ================= MMA issue ======================================================
+  } else if (warp == 1 || (NT == 2 && warp == 3)) {
+    // ================= MMA issue of tile i ============================================
     // The whole warp walks, one elected lane issues: with warp-uniform control flow the
     // operands stay in uniform registers.  Issued from a branch that one lane takes, every
-    // MMA first moved its five operands there, and cost 85-140 cycles instead of 64.
+    // MMA first moved its five operands there, and cost 85-140 cycles instead of 64.  A warp a
+    // tile: the barriers and commits of one cost as much as its products take (1.4 k of 3.4 k
+    // cycles a half block of two tiles when one warp did both).
+    const int i = warp >> 1;
     const uint32_t lead = elect_one();
-    constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, 0);
+    constexpr uint32_t ID_QK = idesc_bf16_f32(128, 64, 0);
     constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, 1);
-    const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+    const uint64_t dq = smem_desc_sw128(sQ + i * C::Q_BYTES, 16, 1024);
     const uint64_t dk = smem_desc_sw128(sK, 16, 1024);
     const uint64_t dv = smem_desc_sw128(sV, C::KB * 128, 1024);
-    // S buffer sbuf = Q tile i times the K block in slot s
-    auto qk = [&](int i, int sbuf, int s) {
-      uint64_t dqi = dq + ((uint32_t)i * C::Q_BYTES >> 4);
-      uint64_t dks = dk + ((uint32_t)s * C::BLK_BYTES >> 4);
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_ss_if(lead, tmem + sbuf * 128, dqi + 2 * k, dks + 2 * k, ID_QK,
-                         (h > 0 || k > 0) ? 1u : 0u);
-        dqi += (128 * 128) >> 4;
-        dks += (C::KB * 128) >> 4;
-      }
-      mma_commit_if(lead, b_sfull(sbuf));
-    };
-    int it = 0, seg = 0, cnt1 = 0;  // blocks of the CTA (and tile 0), segments, blocks of tile 1
+    const uint32_t t_s = tmem + i * 128, t_o = tmem + C::COL_O + i * D;
+    int it = 0, seg = 0, cnt = 0;  // blocks of the CTA, segments, half blocks of the tile
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
-    auto kwait = [&](int x) { return all(wait(b_kfull(x % C::KS), (x / C::KS) & 1)); };
     for (; ok; ++seg) {
       if (!all(walk.next(prm.tiles, prm.cum))) break;
       const int nb = __shfl_sync(0xffffffffu, walk.nb, 0);
       const int keys0 = __shfl_sync(0xffffffffu, walk.tile.kv - walk.jb * C::KB, 0);
-      const int nt = NT == 2 && all(walk.tile.ntok > TOK) ? 2 : 1;
       if (!all(wait(b_qfull, seg & 1))) { ok = false; break; }
-      // Step j: the products P V of block j - 1 and Q K^T of block j, in the order
-      //   NT = 2:  PV0(j-1) QK0(j) | PV1(j-1) QK1(j)
-      //   NT = 1:  QK(j) | PV(j-1), the scores under the softmax of the block before
-      for (int j = 0; j <= nb; ++j) {
-        const int vs = (it + j - 1 + C::VS) % C::VS, ks = (it + j) % C::KS;
-        if (j < nb) {
-          if (!kwait(it + j)) { ok = false; break; }
-          tc_fence_after();
+      if (i == 1 && all(walk.tile.ntok <= TOK)) {
+        // no second tile here: hand every slot on once it has been filled (not before: an
+        // arrival ahead of the slot's phase would count for an earlier one)
+        if (lane == 0) mbar_arrive(b_qempty);
+        for (int x = it; ok && x < it + nb; ++x) {
+          ok = all(wait(b_kfull(x % C::KS), (x / C::KS) & 1));
+          if (ok && lane == 0) mbar_arrive(b_kempty(x % C::KS));
+          ok = ok && all(wait(b_vfull(x % C::VS), (x / C::VS) & 1));
+          if (ok && lane == 0) mbar_arrive(b_vempty(x % C::VS));
         }
-        if (NT == 1 && j < nb) qk(0, (it + j) & 1, ks);
-        if (j > 0 && !all(wait(b_vfull(vs), ((it + j - 1) / C::VS) & 1))) { ok = false; break; }
-        const int keys = keys0 - (j - 1) * C::KB;
-        // one copy for both tiles: the issue loop has to stay in the instruction cache, but its
-        // steps want to be unrolled (chunk of 2048 on 32K keys: 1.08 ms so, 1.16 ms with both
-        // tiles unrolled, 1.21 ms with the steps rolled)
-#pragma unroll 1
-        for (int i = 0; i < nt; ++i) {
-          if (j > 0) {
-            const int sbuf = NT == 1 ? (it + j - 1) & 1 : i;
-            const uint32_t ph = (NT == 1 ? (it + j - 1) >> 1 : (i == 0 ? it + j - 1 : cnt1)) & 1;
-            uint64_t dvs = dv + ((uint32_t)vs * C::BLK_BYTES >> 4);
-            uint32_t t_p = tmem + sbuf * 128;
-            // O of tile i (+)= P V, 64 keys as soon as their P is there
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!all(wait_hot(b_pfull(sbuf, h), ph))) { ok = false; break; }
+      } else {
+        const int ns = half_blocks(nb, keys0);
+        // Step n: S(n) = Q K(n)^T, then O += P(n - 1) V(n - 1): the scores of a half block come in
+        // under the softmax of the one before
+        for (int n = 0; n <= ns; ++n) {
+          if (n < ns) {
+            const int x = it + (n >> 1), s = x % C::KS, buf = (cnt + n) & 1;
+            if (!(n & 1)) {
+              if (!all(wait(b_kfull(s), (x / C::KS) & 1))) { ok = false; break; }
               tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_ts_if(h * 64 + k * 16 < keys ? lead : 0u, tmem + C::COL_O + i * D,
-                               t_p + k * 8, dvs + ((k * 16 * 128) >> 4), ID_PV,
-                               (j > 1 || h > 0 || k > 0) ? 1u : 0u);
-              dvs += (64 * 128) >> 4;
-              t_p += 32;
             }
-            if (!ok) break;
-            if (i == 1) ++cnt1;
-            if (NT == 1) mma_commit_if(lead, b_pv);
-            if (j == nb) mma_commit_if(lead, b_ofull(i));
+            const uint64_t dks = dk + (((uint32_t)s * C::BLK_BYTES + (n & 1) * (64 * 128)) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_bf16_ss_if(lead, t_s + buf * 64, dq + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                             dks + (((k >> 2) * (C::KB * 128) + (k & 3) * 32) >> 4), ID_QK,
+                             k > 0 ? 1u : 0u);
+            mma_commit_if(lead, b_sfull(i, buf));
+            if ((n & 1) || n + 1 == ns) mma_commit_if(lead, b_kempty(s));
+            if (n + 1 == ns) mma_commit_if(lead, b_qempty);
           }
-          if (NT == 2 && j < nb) qk(i, i, ks);
+          if (n > 0) {
+            const int m = n - 1, x = it + (m >> 1), s = x % C::VS, c = cnt + m, buf = c & 1;
+            if (!(m & 1) && !all(wait(b_vfull(s), (x / C::VS) & 1))) { ok = false; break; }
+            if (!all(wait_hot(b_pfull(i, buf), (c >> 1) & 1))) { ok = false; break; }
+            tc_fence_after();
+            const int keys = keys0 - m * 64;
+            const uint64_t dvs = dv + (((uint32_t)s * C::BLK_BYTES + (m & 1) * (64 * 128)) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ts_if(k * 16 < keys ? lead : 0u, t_o, t_s + buf * 64 + k * 8,
+                             dvs + ((k * 16 * 128) >> 4), ID_PV, (m > 0 || k > 0) ? 1u : 0u);
+            mma_commit_if(lead, b_pv(i));
+            if (n == ns) mma_commit_if(lead, b_ofull(i));
+            if ((m & 1) || n == ns) mma_commit_if(lead, b_vempty(s));
+          }
         }
-        if (!ok) break;
-        if (j > 0) mma_commit_if(lead, b_vempty(vs));
-        if (j < nb) mma_commit_if(lead, b_kempty(ks));
-        if (j == nb - 1) mma_commit_if(lead, b_qempty);
+        cnt += ns;
       }
       if (!ok) break;
       it += nb;
       walk.advance();
     }
     // every issued MMA completes before teardown frees TMEM
-    mma_commit_if(lead, b_done);
+    mma_commit_if(lead, b_done(i));
     const uint64_t t0 = globaltimer_ns();
-    if (lane == 0) drain_wait(b_done, 0, t0, tmo);
+    if (lane == 0) drain_wait(b_done(i), 0, t0, tmo);
   }
   } else {
     // ================= softmax of tile i, one row per thread ==========================
@@ -553,187 +551,136 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t t_o = t_row + C::COL_O + i * D;
     const int row_tok = row / G, row_g = row - row_tok * G;
-    int cnt = 0, it = 0, nseg = 0;  // blocks of this tile / of the CTA, segments of this tile
+    int cnt = 0, nseg = 0;  // half blocks and segments of this tile
     bool ok = true;
-    for (; ok && walk.next(prm.tiles, prm.cum); it += walk.nb, walk.advance()) {
+    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance()) {
       const int ntok = walk.tile.ntok - i * TOK;
       if (ntok <= 0) continue;  // a lone tile: the second group of warps has no rows
       const int token = walk.tile.tok0 + i * TOK + row_tok;
       const int pos = walk.tile.pos0 + i * TOK + row_tok;
       const bool row_valid = row_tok < min(TOK, ntok);
       const int head = walk.hk * G + row_g;
-      int lo = 0, hi = -1;
+      int lo = INT_MIN, hi = INT_MAX;  // rows without a token need no mask: their result goes nowhere
       float slope = 0.f;
       if (row_valid) {
         token_range(prm.mask, token, pos, walk.tile.kv, walk.tile.prefix, lo, hi);
         if (BIAS) slope = __ldg(prm.slopes + head) * 1.4426950408889634f;
       }
       const bool warp_works = __any_sync(0xffffffffu, row_valid);
+      // the keys that every row of the warp sees: [alo, ahi]
+      const int alo = __reduce_max_sync(0xffffffffu, lo), ahi = __reduce_min_sync(0xffffffffu, hi);
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < walk.nb; ++j, ++cnt) {
-        const int sbuf = NT == 1 ? cnt & 1 : i;
-        const uint32_t t_s = t_row + sbuf * 128;
-        if (!wait_warp_hot(b_sfull(sbuf), (NT == 1 ? cnt >> 1 : cnt) & 1)) { ok = false; break; }
+      const int ns = half_blocks(walk.nb, walk.tile.kv - walk.jb * C::KB);
+      for (int n = 0; n < ns; ++n, ++cnt) {
+        const int buf = cnt & 1;
+        const uint32_t t_s = t_row + i * 128 + buf * 64;
+        if (!wait_warp_hot(b_sfull(i, buf), (cnt >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
-        const int key0 = (walk.jb + j) * C::KB;
-        // rows without a token never need the mask: their result goes nowhere
-        const bool inside = !row_valid || (lo <= key0 && hi >= key0 + C::KB - 1);
-        // one barrier a buffer: with one tile a warp without rows may be a block ahead of the
-        // others, and its arrival must not count for theirs
-        auto hand_over = [&](int h) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_pfull(sbuf, h));
-        };
+        const int key0 = walk.jb * C::KB + n * 64;
         if (warp_works) {
-          const bool whole_block = __all_sync(0xffffffffu, inside);
-          const int rlo = lo - key0, rhi = hi - key0;
-          const float dist0 = (float)(key0 - pos);
-          // scores of columns c + 2e, c + 2e + 1 in log2 units, plus `add`
-          auto pair = [&](auto small_tag, const uint32_t* v, int c, int e, f32x2 add) -> f32x2 {
-            f32x2 x = score2_log2<CAP, decltype(small_tag)::value>(
-                prm.score, pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), add);
-            if (BIAS) {
-              float d0, d1;
-              unpack2(add2(both(dist0 + (float)c), pack2((float)(2 * e), (float)(2 * e + 1))), d0, d1);
-              x = fma2(both(-slope), pack2(fabsf(d0), fabsf(d1)), x);
-            }
-            return x;
-          };
-          // one bit a column of [c, c + 32): seen
-          auto seen_bits = [&](int c) -> uint32_t {
-            const int b0 = max(rlo - c, 0), b1 = min(rhi - c, 31);
-            return b0 > b1 ? 0u : (0xffffffffu << b0) & (0xffffffffu >> (31 - b1));
-          };
-          // f(v, c) for the row's columns, 32 at a time, the next ones loading meanwhile
-          auto pieces = [&](auto f) {
-            uint32_t va[32], vb[32];
-            tmem_ld32_async(t_s, va);
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
-              tmem_ld_wait32(va);
-              tmem_ld32_async(t_s + c + 32, vb);
-              f(va, c);
-              tmem_ld_wait32(vb);
-              if (!c) tmem_ld32_async(t_s + 64, va);
-              f(vb, c + 32);
-            }
-          };
-          // ---- row max.  Without a bias the cap and the scale are monotone: raw products do
-          float m_loc, far = 0.f;  // far: the largest |product| seen (capped scores)
-          if (!BIAS && whole_block) {
-            uint32_t sa[64], sb[64];
-            tmem_ld64_async(t_s, sa);
-            tmem_ld64_async(t_s + 64, sb);
-            tmem_ld_wait64x2(sa, sb);
-            float a[4], z[4];
+          uint32_t sc[64];
+          tmem_ld64(t_s, sc);
+          const bool plain = alo <= key0 && ahi >= key0 + 63;
+          // ---- scores in log2 units where they are shaped (otherwise the scale goes into the
+          // exponent below), the unseen ones -inf
+          if (CAP) {
+            float far = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[e] = fmaxf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
-              if (CAP) z[e] = fminf(__uint_as_float(sa[e]), __uint_as_float(sa[e + 4]));
-            }
+            for (int e = 0; e < 64; e += 2)
+              far = fmax3f(far, fabsf(__uint_as_float(sc[e])), fabsf(__uint_as_float(sc[e + 1])));
+            auto shape = [&](auto small_tag) {
 #pragma unroll
-            for (int e = 8; e < 128; e += 8)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float u = __uint_as_float(e < 64 ? sa[e + 2 * x] : sb[e - 64 + 2 * x]);
-                const float w = __uint_as_float(e < 64 ? sa[e + 2 * x + 1] : sb[e - 64 + 2 * x + 1]);
-                a[x] = fmax3f(a[x], u, w);
-                if (CAP) z[x] = fmin3f(z[x], u, w);
-              }
-            m_loc = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-            if (CAP) far = fmaxf(fabsf(m_loc), fabsf(fminf(fminf(z[0], z[1]), fminf(z[2], z[3]))));
-            m_loc = score_log2<CAP>(prm.score, m_loc);
-          } else {
-            float a[2] = {-INFINITY, -INFINITY};
-            pieces([&](const uint32_t* v, int c) {
-              const uint32_t bits = whole_block ? 0xffffffffu : seen_bits(c);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x0 = __uint_as_float(v[2 * e]), x1 = __uint_as_float(v[2 * e + 1]);
-                if (CAP) far = fmaxf(far, fmaxf((bits >> (2 * e)) & 1u ? fabsf(x0) : 0.f,
-                                                (bits >> (2 * e + 1)) & 1u ? fabsf(x1) : 0.f));
-                if (BIAS) unpack2(pair(std::false_type{}, v, c, e, both(0.f)), x0, x1);
-                if (!((bits >> (2 * e)) & 1u)) x0 = -INFINITY;
-                if (!((bits >> (2 * e + 1)) & 1u)) x1 = -INFINITY;
-                a[e & 1] = fmax3f(a[e & 1], x0, x1);
-              }
-            });
-            m_loc = fmaxf(a[0], a[1]);
-            if (!BIAS && m_loc != -INFINITY) m_loc = score_log2<CAP>(prm.score, m_loc);
-          }
-          const bool resc = m_loc > m_ref + C::kRescale;
-          if (j > 0 && __any_sync(0xffffffffu, resc)) {
-            if (NT == 1) {  // O is at rest once the previous block's product is done
-              if (!wait_warp(b_pv, (cnt - 1) & 1)) { ok = false; break; }
-              tc_fence_after();
-            }
-            const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t r[16];
-              tmem_ld16(t_o + k * 16, r);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-              tmem_st16(t_o + k * 16, r);
-            }
-            tmem_st_wait();
-            l *= alpha;
-          }
-          if (resc) m_ref = m_loc;
-          const float nb2 = m_ref == -INFINITY ? 0.f : -m_ref;
-          // ---- P = 2^(score - m_ref) as bf16 pairs over the first half of the S columns,
-          // handed to the MMA thread 64 keys at a time.  A rolled loop that reads S again: the
-          // SM's instruction cache holds all roles' loops only if this one is short (unrolled
-          // over a row held in registers, it missed 22 lines a block and ran a third slower)
-          const f32x2 nb22 = both(nb2);
-          f32x2 sum[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = both(0.f);
-          auto weights = [&](auto mask_tag, auto small_tag) {
-            pieces([&](const uint32_t* v, int c) {
-              constexpr bool MASK = decltype(mask_tag)::value;
-              const uint32_t bits = MASK ? seen_bits(c) : 0u;
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < 64; e += 2) {
                 float x0, x1;
-                unpack2(pair(small_tag, v, c, e, nb22), x0, x1);
-                if (MASK) {
-                  if (!((bits >> (2 * e)) & 1u)) x0 = -INFINITY;
-                  if (!((bits >> (2 * e + 1)) & 1u)) x1 = -INFINITY;
-                }
-                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
-                __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
-                w[e] = *reinterpret_cast<uint32_t*>(&v2);
+                unpack2(score2_log2<true, decltype(small_tag)::value>(
+                            prm.score, pack2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])),
+                            both(0.f)),
+                        x0, x1);
+                sc[e] = __float_as_uint(x0);
+                sc[e + 1] = __float_as_uint(x1);
               }
-              tmem_st16(t_s + (c >> 1), w);
-              if (c == 64) {  // the first half's stores have had a quarter's time to land
-                tmem_st_wait();
-                hand_over(0);
-              }
-            });
-          };
-          const bool small = CAP && __all_sync(0xffffffffu, !row_valid || far <= prm.score.lim);
-          if (whole_block) {
-            if (small) weights(std::false_type{}, std::true_type{});
-            else weights(std::false_type{}, std::false_type{});
-          } else {
-            if (small) weights(std::true_type{}, std::true_type{});
-            else weights(std::true_type{}, std::false_type{});
+            };
+            if (__all_sync(0xffffffffu, !row_valid || far <= prm.score.lim)) shape(std::true_type{});
+            else shape(std::false_type{});
           }
-          tmem_st_wait();
-          hand_over(1);
-          const f32x2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          if (BIAS) {
+            const f32x2 d0 = both((float)(key0 - pos)), mul = both(CAP ? 1.f : prm.score.a);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              float a0, a1;
+              unpack2(add2(d0, pack2((float)e, (float)(e + 1))), a0, a1);
+              const f32x2 x = mul2(pack2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), mul);
+              unpack2(fma2(both(-slope), pack2(fabsf(a0), fabsf(a1)), x), a0, a1);
+              sc[e] = __float_as_uint(a0);
+              sc[e + 1] = __float_as_uint(a1);
+            }
+          }
+          if (!plain) {
+            const int r0 = max(lo - key0, 0), r1 = min(hi - key0, 63);  // one bit a column: seen
+            const uint64_t bits = r0 > r1 ? 0ull : (~0ull << r0) & (~0ull >> (63 - r1));
+            const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (!(((e < 32 ? b0 : b1) >> (e & 31)) & 1u)) sc[e] = 0xff800000u;  // -inf
+          }
+          // ---- row max
+          float a[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(sc[e]), __uint_as_float(sc[e + 4]));
+#pragma unroll
+          for (int e = 8; e < 64; e += 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              a[x] = fmax3f(a[x], __uint_as_float(sc[e + 2 * x]), __uint_as_float(sc[e + 2 * x + 1]));
+          const float m_loc = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * (CAP || BIAS ? 1.f : prm.score.a);
+          const bool resc = m_loc > m_ref + C::kRescale;
+          if (__any_sync(0xffffffffu, resc)) {
+            if (n > 0) {  // O is at rest once the previous half block's product is done
+              if (!wait_warp(b_pv(i), (cnt - 1) & 1)) { ok = false; break; }
+              tc_fence_after();
+              const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t r[16];
+                tmem_ld16(t_o + k * 16, r);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st16(t_o + k * 16, r);
+              }
+              l *= alpha;
+            }
+            if (resc) m_ref = m_loc;
+          }
+          // ---- P = 2^(score - m_ref) as bf16 pairs over the first half of the S columns
+          const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
+          const f32x2 nb2 = both(nb), mul = both(prm.score.a);
+          f32x2 sum[2] = {both(0.f), both(0.f)};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              f32x2 x = pack2(__uint_as_float(sc[32 * c + 2 * e]), __uint_as_float(sc[32 * c + 2 * e + 1]));
+              x = (CAP || BIAS) ? add2(x, nb2) : fma2(x, mul, nb2);
+              float x0, x1;
+              unpack2(x, x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+              __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+              w[e] = *reinterpret_cast<uint32_t*>(&v2);
+            }
+            tmem_st16(t_s + c * 16, w);
+          }
           float t0, t1;
-          unpack2(t, t0, t1);
+          unpack2(add2(sum[0], sum[1]), t0, t1);
           l += t0 + t1;
-        } else {
-          hand_over(0);
-          hand_over(1);
+          tmem_st_wait();
         }
-        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        // one barrier a buffer: a warp without rows may be a half block ahead of the others, and
+        // its arrival must not count for theirs
+        if (lane == 0) mbar_arrive(b_pfull(i, buf));
       }
       // ---- epilogue: O / l, or the partial rows of a tile cut between CTAs
       const bool have = ok && wait_warp(b_ofull(i), nseg & 1);
