@@ -334,13 +334,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     if (lane == 0) okl = wait(bar_addr, parity) ? 1 : 0;
     return __shfl_sync(0xffffffffu, okl, 0) != 0;
   };
-  // the same without suspending: for the hand-offs on the softmax / MMA cycle
-  auto wait_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-    return mbar_test_wait(bar_addr, parity) || wait_on_hot(bar_addr, parity, abort_at, tmo);
-  };
+  // the same without suspending: for the softmax's wait, which starts its cycle (the MMA warps
+  // suspend: their polling took issue slots and, under the power cap, clock)
   auto wait_warp_hot = [&](uint32_t bar_addr, uint32_t parity) -> bool {
     int okl = 1;
-    if (lane == 0) okl = wait_hot(bar_addr, parity) ? 1 : 0;
+    if (lane == 0)
+      okl = mbar_test_wait(bar_addr, parity) || wait_on_hot(bar_addr, parity, abort_at, tmo) ? 1 : 0;
     return __shfl_sync(0xffffffffu, okl, 0) != 0;
   };
   const int pshift = 31 - __clz(P);        // P is a power of two
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           if (n > 0) {
             const int m = n - 1, x = it + (m >> 1), s = x % C::VS, c = cnt + m, buf = c & 1;
             if (!(m & 1) && !all(wait(b_vfull(s), (x / C::VS) & 1))) { ok = false; break; }
-            if (!all(wait_hot(b_pfull(i, buf), (c >> 1) & 1))) { ok = false; break; }
+            if (!all(wait(b_pfull(i, buf), (c >> 1) & 1))) { ok = false; break; }
             tc_fence_after();
             const int keys = keys0 - m * 64;
             const uint64_t dvs = dv + (((uint32_t)s * C::BLK_BYTES + (m & 1) * (64 * 128)) >> 4);
@@ -640,12 +639,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
               tc_fence_after();
               const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
 #pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) {
-                uint32_t r[16];
-                tmem_ld16(t_o + k * 16, r);
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t r[32];
+                tmem_ld32(t_o + k * 32, r);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                tmem_st16(t_o + k * 16, r);
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st32(t_o + k * 32, r);
               }
               l *= alpha;
             }
