@@ -1465,12 +1465,14 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the largest segment's keys, where they fit beside the static histograms
   const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
-  p.seg_cap = seg <= EVICT_SEG_MAX ? seg : 0;
-  const size_t smem = (size_t)p.seg_cap * sizeof(uint32_t);
-  e = allow_smem<evict_select_kernel>(EVICT_SEG_MAX * (int)sizeof(uint32_t));
-  if (e != COSA_OK) return e;
-  evict_select_kernel<<<dim3(EVICT_CL, shape->num_kv_heads, shape->batch), EVICT_THREADS, smem,
-                        st>>>(p);
+  dim3 clusters(EVICT_CL, shape->num_kv_heads, shape->batch);
+  if (seg <= EVICT_SEG_MAX) {
+    e = allow_smem<evict_select_kernel<true>>(EVICT_SEG_MAX * (int)sizeof(uint32_t));
+    if (e != COSA_OK) return e;
+    evict_select_kernel<true><<<clusters, EVICT_THREADS, (size_t)seg * sizeof(uint32_t), st>>>(p);
+  } else {
+    evict_select_kernel<false><<<clusters, EVICT_THREADS, 0, st>>>(p);
+  }
   e = last_launch();
   if (e != COSA_OK) return e;
   const int most = evict->budget < shape->max_kv ? evict->budget : shape->max_kv;

@@ -30,7 +30,6 @@ struct EvictParams {
   long long mass_stride;
   int num_kv_heads, page_size, pages_per_seq, num_phys_pages, max_kv, dst_pages;
   int budget, sink, recent;
-  int seg_cap;  // keys of a segment that the selection holds in shared memory
 };
 
 constexpr int EVICT_CL = 8;
@@ -106,8 +105,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32
   return before + inc - v;
 }
 
-// Dynamic shared memory: the segment's keys, p.seg_cap words (0: they are read again from
-// the masses in every pass, for caches past 8 * 40960 keys).
+// HELD: the segment's keys are kept in dynamic shared memory; else they are read again from
+// the masses in every pass (caches past 8 * 40960 keys).
+template <bool HELD>
 __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS)
     evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys_s[];
@@ -141,12 +141,11 @@ __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS
   const int seg = (m + EVICT_CL - 1) / EVICT_CL;
   const int s0 = min(rank * seg, m), n = min(s0 + seg, m) - s0;
   const float* mass = p.mass + bh * p.mass_stride + p.sink + s0;
-  const bool held = seg <= p.seg_cap;
-  auto key = [&](int i) { return held ? keys_s[i] : mass_key(__ldg(mass + i)); };
+  auto key = [&](int i) { return HELD ? keys_s[i] : mass_key(__ldg(mass + i)); };
   for (int i = tid; i < 3 * EVICT_BINS / 4; i += EVICT_THREADS)
     reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int i = tid; i < 3 * EVICT_SLICE; i += EVICT_THREADS) sums[0][i] = 0u;
-  if (held) {
+  if (HELD) {
     int i = tid;
     for (; i + 7 * EVICT_THREADS < n; i += 8 * EVICT_THREADS) {
       float v[8];
@@ -163,28 +162,37 @@ __global__ void __cluster_dims__(EVICT_CL, 1, 1) __launch_bounds__(EVICT_THREADS
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
-    for (int i0 = 0; i0 < n; i0 += EVICT_THREADS) {
-      const int i = i0 + tid;
-      const uint32_t k = i < n ? key(i) : 0u;
-      const bool in = i < n && (pass == 0 || (k >> (shift + bits)) == prefix);
-      // masses of exactly zero (keys that no token has seen) come in numbers: a warp counts
-      // its own with one addition
-      const uint32_t zero = __ballot_sync(0xffffffffu, in && k == 0x80000000u);
-      const bool mine = in && (k != 0x80000000u || lane == __ffs(zero) - 1);
-      if (mine)
-        atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1u)],
-                  k == 0x80000000u ? (uint32_t)__popc(zero) : 1u);
+    const int top = shift + bits;
+    uint32_t* h = hist[pass];
+    const uint32_t mask = (1u << bits) - 1u;
+    if (pass == 0 || prefix == 0x80000000u >> top) {
+      // masses of exactly zero (keys that no token has seen) come in numbers: a warp counts its
+      // own with one addition
+      for (int i0 = 0; i0 < n; i0 += EVICT_THREADS) {
+        const int i = i0 + tid;
+        const uint32_t k = i < n ? key(i) : 0u;
+        const bool in = i < n && (pass == 0 || (k >> top) == prefix);
+        const uint32_t zero = __ballot_sync(0xffffffffu, in && k == 0x80000000u);
+        if (in && k != 0x80000000u) atomicAdd(h + ((k >> shift) & mask), 1u);
+        if (zero && lane == 0) atomicAdd(h + ((0x80000000u >> shift) & mask), (uint32_t)__popc(zero));
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += EVICT_THREADS) {
+        const uint32_t k = key(i);
+        if ((k >> top) == prefix) atomicAdd(h + ((k >> shift) & mask), 1u);
+      }
     }
     __syncthreads();
     // a thread's four bins into the slices that their owners hold; few are not empty
     const int bin0 = EVICT_BINS - 4 - 4 * tid;
-    const uint4 h = *reinterpret_cast<const uint4*>(&hist[pass][bin0]);
+    const uint4 own = *reinterpret_cast<const uint4*>(&hist[pass][bin0]);
     uint32_t* at = &sums[pass][bin0 % EVICT_SLICE];
     const int owner = bin0 / EVICT_SLICE;
-    if (h.x) add_cluster(at, owner, h.x);
-    if (h.y) add_cluster(at + 1, owner, h.y);
-    if (h.z) add_cluster(at + 2, owner, h.z);
-    if (h.w) add_cluster(at + 3, owner, h.w);
+    if (own.x) add_cluster(at, owner, own.x);
+    if (own.y) add_cluster(at + 1, owner, own.y);
+    if (own.z) add_cluster(at + 2, owner, own.z);
+    if (own.w) add_cluster(at + 3, owner, own.w);
     cluster_sync();
     // from the largest digit down: the digit at which `want` keys are reached
     const uint4 t4 = ld_cluster4(at, owner);
