@@ -740,9 +740,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 
 // ---- join of the tiles that were cut ----------------------------------------------------
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_DEEP = 16;  // loads of a row in flight: the join is all latency
+constexpr int JOIN_ROWS = 4;  // rows of a warp, JOIN_WARPS apart
 
-// grid (NUM_SMS, row groups); one row a warp
+// grid (NUM_SMS, groups of JOIN_WARPS * JOIN_ROWS rows).  All latency: the loads of all a warp's
+// rows (a prompt's tile: two or three parts each) or of 16 parts of one row (a decode step's)
+// are in flight together.
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const ChunkAttnParams p) {
   constexpr int EPL = D / 32;  // floats a lane
@@ -750,61 +752,108 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
   const int4 jn = __ldcg(reinterpret_cast<const int4*>(p.joins + blockIdx.x));
   if (!jn.x) return;  // ntok = 0: this CTA cut no tile
   const int last = __ldcg(&p.joins[blockIdx.x].last);
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
-  const int G = p.group, r = row & 127;
-  const int tok = (row >> 7) * p.tile_tokens + r / G;
-  if (r >= p.tile_tokens * G || tok >= jn.x) return;
+  const int lane = threadIdx.x & 31, G = p.group;
   const int c0 = blockIdx.x, n = last - c0 + 1;
-  auto slot = [&](int s) { return (long long)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.part_rows + row; };
-  float l = 0.f, m = -INFINITY, o[EPL];
+  const int row0 = blockIdx.y * (JOIN_WARPS * JOIN_ROWS) + (threadIdx.x >> 5);
+  auto tok_of = [&](int row) { return (row >> 7) * p.tile_tokens + (row & 127) / G; };
+  auto real = [&](int row) {
+    return row < p.part_rows && (row & 127) < p.tile_tokens * G && tok_of(row) < jn.x;
+  };
+  auto slot = [&](int s, int row) {
+    return (long long)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.part_rows + row;
+  };
+  auto load = [&](long long at, float* v) {
+    const float* src = p.part_o + at * D + lane * EPL;
+    if (EPL == 4) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+      v[0] = t.x, v[1] = t.y, v[EPL - 2] = t.z, v[EPL - 1] = t.w;
+    } else {
+      const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+      v[0] = t.x, v[1] = t.y;
+    }
+  };
+  auto finish = [&](int row, float m, float l, const float* o) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long out =
+        (long long)(jn.y + tok_of(row)) * p.num_q_heads + jn.z * G + (row & 127) % G;
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  // 32 parts at a time: a lane holds one part's base and sum, the rows come many loads deep
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const int cnt = min(32, n - s0);
-    const float2 ml = lane < cnt ? __ldcg(p.part_ml + slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
-    const float mx = fmaxf(m, warp_max(ml.x));
-    if (mx == -INFINITY) continue;
-    const float back = tc::ex2_approx(m - mx);  // (from -inf: 0)
-    const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - mx) : 0.f;
-    float part = w * ml.y;
+    for (int e = 0; e < EPL; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(p.out + out * D + lane * EPL + e) =
+          __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    if (p.lse && lane == 0)
+      p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  };
+  if (n <= 3) {
+    float2 ml[JOIN_ROWS][3];
+    float v[JOIN_ROWS][3][EPL];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
-    l = fmaf(l, back, part);
-    m = mx;
+    for (int k = 0; k < JOIN_ROWS; ++k)
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] *= back;
-    for (int s = 0; s < cnt; s += JOIN_DEEP) {
-      float v[JOIN_DEEP][EPL];
-#pragma unroll
-      for (int x = 0; x < JOIN_DEEP; ++x) {
-        const float* src = p.part_o + slot(s0 + min(s + x, cnt - 1)) * D + lane * EPL;
-        if (EPL == 4) {
-          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-          v[x][0] = t.x, v[x][1] = t.y, v[x][EPL - 2] = t.z, v[x][EPL - 1] = t.w;
-        } else {
-          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-          v[x][0] = t.x, v[x][1] = t.y;
+      for (int s = 0; s < 3; ++s) {
+        ml[k][s] = make_float2(-INFINITY, 0.f);
+        if (s < n && real(row0 + k * JOIN_WARPS)) {
+          const long long at = slot(s, row0 + k * JOIN_WARPS);
+          ml[k][s] = __ldcg(p.part_ml + at);
+          load(at, v[k][s]);
         }
       }
 #pragma unroll
-      for (int x = 0; x < JOIN_DEEP; ++x) {
-        const float ws = __shfl_sync(0xffffffffu, w, min(s + x, 31));
-        if (s + x < cnt && ws > 0.f)  // (a part without keys has no weight, whatever its O holds)
+    for (int k = 0; k < JOIN_ROWS; ++k) {
+      if (!real(row0 + k * JOIN_WARPS)) continue;
+      const float m = fmaxf(fmaxf(ml[k][0].x, ml[k][1].x), ml[k][2].x);
+      float l = 0.f, o[EPL];
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) o[e] = fmaf(ws, v[x][e], o[e]);
+      for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+        if (ml[k][s].y > 0.f) {  // (a part without keys has no weight, whatever its O holds)
+          const float w = tc::ex2_approx(ml[k][s].x - m);
+          l = fmaf(w, ml[k][s].y, l);
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, v[k][s][e], o[e]);
+        }
+      finish(row0 + k * JOIN_WARPS, m, l, o);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int k = 0; k < JOIN_ROWS; ++k) {
+    const int row = row0 + k * JOIN_WARPS;
+    if (!real(row)) continue;
+    float l = 0.f, m = -INFINITY, o[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+    // 32 parts at a time: a lane holds one part's base and sum
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const int cnt = min(32, n - s0);
+      const float2 ml =
+          lane < cnt ? __ldcg(p.part_ml + slot(s0 + lane, row)) : make_float2(-INFINITY, 0.f);
+      const float mx = fmaxf(m, warp_max(ml.x));
+      if (mx == -INFINITY) continue;
+      const float back = tc::ex2_approx(m - mx);  // (from -inf: 0)
+      const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - mx) : 0.f;
+      float part = w * ml.y;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+      l = fmaf(l, back, part);
+      m = mx;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] *= back;
+      for (int s = 0; s < cnt; s += 16) {
+        float v[16][EPL];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) load(slot(s0 + min(s + x, cnt - 1), row), v[x]);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const float ws = __shfl_sync(0xffffffffu, w, min(s + x, 31));
+          if (s + x < cnt && ws > 0.f)
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) o[e] = fmaf(ws, v[x][e], o[e]);
+        }
       }
     }
+    finish(row, m, l, o);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const long long out = (long long)(jn.y + tok) * p.num_q_heads + jn.z * G + r % G;
-#pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(p.out + out * D + lane * EPL + e) =
-        __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace cosa

@@ -583,7 +583,7 @@ cosa_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
 template <int D>
 cosa_status_t launch_join(const ChunkAttnParams& prm, cudaStream_t st) {
   return launch_pdl(chunk_combine_kernel<D>,
-                    dim3(NUM_SMS, (prm.part_rows + JOIN_WARPS - 1) / JOIN_WARPS), 32 * JOIN_WARPS,
+                    dim3(NUM_SMS, (prm.part_rows + JOIN_WARPS * JOIN_ROWS - 1) / (JOIN_WARPS * JOIN_ROWS)), 32 * JOIN_WARPS,
                     0, st, prm);
 }
 
