@@ -1,15 +1,15 @@
 // Attention of a few new tokens a sequence over the paged cache: the decode form of
-// cosa_chunk_attention, for at most 32 rows (token, query head) of a sequence and KV head and
+// cosa_chunk_attention, for at most 16 rows (token, query head) of a sequence and KV head and
 // D = 128.
 //
 // Both products are taken transposed, so that the 128-row side of the tensor core holds keys
 // and head dims instead of rows that do not exist:
-//   S^T = K Q^T      128 keys x N rows    (N = 16 or 32)
-//   O^T = V^T P^T    128 dims x N rows,   V^T read from V as it lies (MN-major A)
-// The 128-row form spends 16 / N times the multiplications (and, under the power cap that a
-// stream of the whole cache alone comes near, the clock with them), and leaves the softmax of a
+//   S^T = K Q^T      128 keys x 16 rows
+//   O^T = V^T P^T    128 dims x 16 rows,   V^T read from V as it lies (MN-major A)
+// The tiled form spends eight times the multiplications on this (and, under the power cap that
+// a stream of the whole cache alone comes near, clock with them), and leaves the softmax of a
 // block to the one warp whose rows exist; here a thread owns a key, 128 threads share the
-// block, and P goes to the second product through shared memory (N x 128 bf16).
+// block, and P goes to the second product through shared memory (16 x 128 bf16).
 //
 // The running maximum of a row spans threads: a warp reduces its keys' maxima (one redux a
 // row), the four warps vote whether any row passed its exponent base by 2^8, and only then
@@ -21,16 +21,21 @@
 //   warp 0  Q and K loads     warp 2  V loads, zeroing of the values behind the end, join list
 //   warp 1  MMA issue         warp 3  TMEM allocation
 //   warps 4-7  softmax, one key per thread
-// Bound by the K and V bytes.  Every wait is bounded; a softmax warp whose wait ran out keeps
-// meeting the others at the named barrier.
+// Bound by the K and V bytes over many blocks: 32 ragged sequences of up to 32K keys (7 rows,
+// 1.29 GB) take 198-205 us, 0.96-0.99 of a copy's rate; the tiled form 202 us in short runs and
+// 231 us in long ones, where the clock gives way.  One sequence of 2,049 keys (32 / 8 heads) is
+// latency: 7 us to the partial rows and 12 us joined, of which the first K tile's way through
+// the cold cache and the instructions' own fetch are most (code of rows that do not exist is
+// left by one jump: jumping from row to row cost 2 us).  Every wait is bounded; a softmax warp
+// whose wait ran out keeps meeting the others at the named barrier.
 #pragma once
 
 #include "chunk_attn.cuh"
 
 namespace cosa {
 
-template <int N>
 struct DecCfg {
+  static constexpr int N = 16;  // rows
   static constexpr int D = 128, KB = 128, THREADS = 256;
   static constexpr uint32_t BLK_BYTES = KB * D * 2;
   static constexpr uint32_t Q_BYTES = N * D * 2;   // two halves of N x 64
@@ -46,8 +51,8 @@ struct DecCfg {
   static constexpr uint32_t OFF_MISC = (OFF_BAR + NBAR * 8 + 15) & ~15u;
   static constexpr uint32_t OFF_ROWS = OFF_MISC + 64;        // lo, hi, slope, pos [2][N]
   static constexpr uint32_t OFF_EXCH = OFF_ROWS + 2 * 4 * N * 4;  // [N][4]
-  static constexpr uint32_t SMEM = OFF_EXCH + N * 16;
-  static constexpr int TMEM_COLS = 128;  // S at 0 and 32, O at 64
+  static constexpr uint32_t SMEM = OFF_EXCH + N * 16 + 1024;  // 1024-byte alignment slack
+  static constexpr int TMEM_COLS = 64;  // S at 0 and 16, O at 32
   static constexpr float kRescale = 8.0f;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -101,17 +106,18 @@ __device__ __forceinline__ ChunkTile decode_tile(const ChunkAttnParams& p, int b
   return d;
 }
 
-template <int N, bool CAP, bool BIAS>
+template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(256, 1)
     chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const ChunkAttnParams prm) {
-  using C = DecCfg<N>;
+  using C = DecCfg;
   using namespace tc;
-  constexpr int D = C::D;
-  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // no other shared memory: 1024-aligned
-  const uint32_t sb0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem_tiles));
-  uint8_t* sg = smem_tiles;
+  constexpr int D = C::D, N = C::N;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+  const uint32_t sb0 = (sraw + 1023u) & ~1023u;
+  uint8_t* sg = smem_raw + (sb0 - sraw);
   const uint32_t sK = sb0 + C::OFF_K, sV = sb0 + C::OFF_V, sQ = sb0 + C::OFF_Q, sP = sb0 + C::OFF_P;
   const uint32_t bar = sb0 + C::OFF_BAR;
   auto b_qfull = [&](int i) { return bar + 8u * i; };
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(256, 1)
           const uint64_t dks = dk + ((uint32_t)s * C::BLK_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_bf16_ss_if(lead, tmem + (x & 1) * 32, dks + (((k >> 2) * (C::KB * 128) + (k & 3) * 32) >> 4),
+            mma_bf16_ss_if(lead, tmem + (x & 1) * 16, dks + (((k >> 2) * (C::KB * 128) + (k & 3) * 32) >> 4),
                            dqs + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), ID_QK, k > 0 ? 1u : 0u);
           mma_commit_if(lead, b_sfull(x & 1));
           mma_commit_if(lead, b_kempty(s));
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(256, 1)
           const uint64_t dps = dp + ((uint32_t)(x & 1) * C::P_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_bf16_ss_if(k * 16 < keys ? lead : 0u, tmem + 64, dvs + ((k * 16 * 128) >> 4),
+            mma_bf16_ss_if(k * 16 < keys ? lead : 0u, tmem + 32, dvs + ((k * 16 * 128) >> 4),
                            dps + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), ID_PV,
                            (j > 1 || k > 0) ? 1u : 0u);
           mma_commit_if(lead, b_pv);
@@ -475,21 +481,18 @@ __global__ void __launch_bounds__(256, 1)
         if (ok) {
           tc_fence_after();
           uint32_t sc[N];
-          if (N == 16) tmem_ld16(t_row + buf * 32, sc);
-          else tmem_ld32(t_row + buf * 32, sc);
+          tmem_ld16(t_row + buf * 16, sc);
           const bool plain = alo <= key0 && ahi >= key0 + C::KB - 1;
 #pragma unroll
           for (int r0 = 0; r0 < N; r0 += 4) {
             if (r0 >= nrow) break;  // one jump past all the code of rows that do not exist
-            {
 #pragma unroll
-              for (int r = r0; r < r0 + 4; ++r) {
-                x[r] = score_log2<CAP>(prm.score, __uint_as_float(sc[r]));
-                if (BIAS) x[r] = fmaf(-rsl[r], fabsf((float)key - rpos[r]), x[r]);
-                if (!plain && (key < rlo[r] || key > rhi[r])) x[r] = -INFINITY;
-                wmax[r] = redux_max(x[r]);
-                grow = grow || (r < nrow && wmax[r] > m_ref[r] + C::kRescale);
-              }
+            for (int r = r0; r < r0 + 4; ++r) {
+              x[r] = score_log2<CAP>(prm.score, __uint_as_float(sc[r]));
+              if (BIAS) x[r] = fmaf(-rsl[r], fabsf((float)key - rpos[r]), x[r]);
+              if (!plain && (key < rlo[r] || key > rhi[r])) x[r] = -INFINITY;
+              wmax[r] = redux_max(x[r]);
+              grow = grow || (r < nrow && wmax[r] > m_ref[r] + C::kRescale);
             }
           }
         }
@@ -528,12 +531,10 @@ __global__ void __launch_bounds__(256, 1)
               if (wait_warp(b_pv, (cnt - 1) & 1)) {
                 tc_fence_after();
                 uint32_t o[N];
-                if (N == 16) tmem_ld16(t_row + 64, o);
-                else tmem_ld32(t_row + 64, o);
+                tmem_ld16(t_row + 32, o);
 #pragma unroll
                 for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
-                if (N == 16) tmem_st16(t_row + 64, o);
-                else tmem_st32(t_row + 64, o);
+                tmem_st16(t_row + 32, o);
                 tmem_st_wait();
               } else {
                 ok = false;
@@ -545,14 +546,12 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
           for (int r0 = 0; r0 < N; r0 += 4) {
             if (r0 >= nrow) break;
-            {
 #pragma unroll
-              for (int r = r0; r < r0 + 4; ++r) {
-                const float p = ex2_approx(x[r] - (m_ref[r] == -INFINITY ? 0.f : m_ref[r]));
-                l[r] += p;
-                st_shared_b16(p_col + buf * C::P_BYTES + r * 128 + ((p_piece ^ (r & 7)) << 4),
-                              __float2bfloat16_rn(p));
-              }
+            for (int r = r0; r < r0 + 4; ++r) {
+              const float p = ex2_approx(x[r] - (m_ref[r] == -INFINITY ? 0.f : m_ref[r]));
+              l[r] += p;
+              st_shared_b16(p_col + buf * C::P_BYTES + r * 128 + ((p_piece ^ (r & 7)) << 4),
+                            __float2bfloat16_rn(p));
             }
           }
           fence_proxy_async_smem();
@@ -567,46 +566,40 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
       for (int r0 = 0; r0 < N; r0 += 4) {
         if (r0 >= nrow) break;
-        {
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-            for (int r = r0; r < r0 + 4; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-          // one 16-byte column of the sums a warp
-          if (lane < 4)
-            exch[(r0 + lane) * 4 + q4] = lane < 2 ? (lane ? l[r0 + 1] : l[r0])
-                                                  : (lane == 2 ? l[r0 + 2] : l[r0 + 3]);
-        }
+          for (int r = r0; r < r0 + 4; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane < 4)
+          exch[(r0 + lane) * 4 + q4] = lane < 2 ? (lane ? l[r0 + 1] : l[r0])
+                                                : (lane == 2 ? l[r0 + 2] : l[r0 + 3]);
       }
       named_bar_sync(1, 128);
       if (ok) {
         tc_fence_after();
         uint32_t o[N];
-        if (N == 16) tmem_ld16(t_row + 64, o);
-        else tmem_ld32(t_row + 64, o);
+        tmem_ld16(t_row + 32, o);
         const long long slot = (2 * blockIdx.x + (wk.part > 0 ? 1 : 0)) * (long long)prm.part_rows;
         long long at = (long long)wk.tile.tok0 * prm.num_q_heads + wk.hk * G;  // row 0's
         int g = 0;
 #pragma unroll
         for (int r = 0; r < N; ++r) {
           if (r >= nrow) break;
-          {
-            const float4 e4 = *reinterpret_cast<const float4*>(exch + r * 4);
-            const float sum = (e4.x + e4.y) + (e4.z + e4.w);
-            if (wk.part < 0) {
-              const float inv = sum > 0.f ? 1.f / sum : 0.f;
-              prm.out[at * D + row] = __float2bfloat16_rn(__uint_as_float(o[r]) * inv);
-              if (prm.lse && row == r)
-                prm.lse[at] = sum > 0.f ? (m_ref[r] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-            } else {
-              prm.part_o[(slot + r) * D + row] = __uint_as_float(o[r]);
-              if (row == r) prm.part_ml[slot + r] = make_float2(m_ref[r], sum);
-            }
-            ++at;  // the next head of the group, or the next token's first
-            if (++g == G) {
-              g = 0;
-              at += prm.num_q_heads - G;
-            }
+          const float4 e4 = *reinterpret_cast<const float4*>(exch + r * 4);
+          const float sum = (e4.x + e4.y) + (e4.z + e4.w);
+          if (wk.part < 0) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            prm.out[at * D + row] = __float2bfloat16_rn(__uint_as_float(o[r]) * inv);
+            if (prm.lse && row == r)
+              prm.lse[at] = sum > 0.f ? (m_ref[r] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          } else {
+            prm.part_o[(slot + r) * D + row] = __uint_as_float(o[r]);
+            if (row == r) prm.part_ml[slot + r] = make_float2(m_ref[r], sum);
+          }
+          ++at;  // the next head of the group, or the next token's first
+          if (++g == G) {
+            g = 0;
+            at += prm.num_q_heads - G;
           }
         }
         tc_fence_before();

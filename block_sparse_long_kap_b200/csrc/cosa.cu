@@ -507,8 +507,9 @@ struct ChunkLayout {
 ChunkLayout chunk_layout(const cosa_chunk_t* s) {
   ChunkLayout L;
   const int G = s->num_q_heads / s->num_kv_heads, tok = 128 / G;
-  // one tile at a time while a sequence's rows fit in it: a pair would leave its second
-  // softmax group idle (one tile with two S buffers keeps the cache stream running)
+  // one tile at a time while a sequence's rows fit in it: the pair's second softmax group would
+  // be idle and a V slot fewer is left.  Measured, one tile against a pair: 20 rows 311 against
+  // 327 us, 64 rows 121 against 124 us (D = 64), 7 rows 184 against 191 us (D = 64)
   L.nt = s->max_q <= tok ? 1 : 2;
   L.part_rows = L.nt == 2 ? 256 : s->max_q * G;
   const size_t span = (size_t)tok * L.nt;
@@ -609,18 +610,18 @@ cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
   return launch_join<D>(prm, st);
 }
 
-template <int N, bool CAP, bool BIAS>
+template <bool CAP, bool BIAS>
 cosa_status_t launch_decode_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm,
                                     const void* q, int64_t q_stride, const void* k_pool,
                                     const void* v_pool, cudaStream_t st) {
-  using Cfg = DecCfg<N>;
+  using Cfg = DecCfg;
   CUtensorMap mq, mk, mv;
   const long long PZ = (long long)s->num_phys_pages * s->num_kv_heads;
   if (!make_map_q(&mq, q, s, q_stride, s->max_q) ||
       !make_map(&mk, k_pool, 128, s->page_size, PZ, s->page_size) ||
       !make_map(&mv, v_pool, 128, s->page_size, PZ, s->page_size))
     return COSA_ERR_CUDA;
-  constexpr auto kern = chunk_decode_kernel<N, CAP, BIAS>;
+  constexpr auto kern = chunk_decode_kernel<CAP, BIAS>;
   cosa_status_t e = allow_smem<kern>((int)Cfg::SMEM);
   if (e != COSA_OK) return e;
   kern<<<NUM_SMS, Cfg::THREADS, Cfg::SMEM, st>>>(mq, mk, mv, prm);
@@ -628,15 +629,14 @@ cosa_status_t launch_decode_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams
   return e != COSA_OK ? e : launch_join<128>(prm, st);
 }
 
-template <int N>
 cosa_status_t launch_decode_chunk(const cosa_chunk_t* s, const ChunkAttnParams& prm, bool cap,
                                   const void* q, int64_t q_stride, const void* k_pool,
                                   const void* v_pool, cudaStream_t st) {
   const bool bias = prm.slopes != nullptr;
-  if (cap && bias) return launch_decode_chunk_t<N, true, true>(s, prm, q, q_stride, k_pool, v_pool, st);
-  if (cap) return launch_decode_chunk_t<N, true, false>(s, prm, q, q_stride, k_pool, v_pool, st);
-  if (bias) return launch_decode_chunk_t<N, false, true>(s, prm, q, q_stride, k_pool, v_pool, st);
-  return launch_decode_chunk_t<N, false, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (cap && bias) return launch_decode_chunk_t<true, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (cap) return launch_decode_chunk_t<true, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+  if (bias) return launch_decode_chunk_t<false, true>(s, prm, q, q_stride, k_pool, v_pool, st);
+  return launch_decode_chunk_t<false, false>(s, prm, q, q_stride, k_pool, v_pool, st);
 }
 
 template <int D, int NT>
@@ -1298,8 +1298,9 @@ cosa_status_t cosa_chunk_write(const cosa_chunk_t* shape, const cosa_rope_params
   p.num_phys_pages = shape->num_phys_pages;
   const long long units = (long long)(Hq + 2 * Hk) * (D / 16);
   if (units > (1 << 26)) return COSA_ERR_UNSUPPORTED;
-  // tokens share a CTA's setup while four CTAs an SM are left; a few tokens are split by
-  // heads instead, one unit a thread
+  // tokens share a CTA's setup while four CTAs an SM are left (8K tokens of 36 heads: 33 us at
+  // four tokens a CTA, 37 at eight, 35 at two); a few tokens are split by heads instead, one
+  // unit a thread (64 tokens of 48 heads: 3.6 against 4.1 us)
   long long tpb = shape->total_q / (4 * NUM_SMS);
   p.tokens_per_cta = tpb < 1 ? 1 : (tpb > 4 ? 4 : (int)tpb);
   const int blocks = (shape->total_q + p.tokens_per_cta - 1) / p.tokens_per_cta;
@@ -1370,12 +1371,11 @@ cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_p
   p.timeout_ns = kWaitTimeoutNs;
   const bool cap = score && score->softcap > 0.f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // A few rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
-  // 32K keys (7 rows): DECODE_NEW against DECODE_OLD us for the 128-row form.
-  const int rows = shape->max_q * p.group;
-  if (shape->head_dim == 128 && rows <= 32)
-    return rows <= 16 ? launch_decode_chunk<16>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
-                      : launch_decode_chunk<32>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
+  // Up to 16 rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
+  // 32K keys, transposed against tiled: 7 rows 198 against 202 us (205 against 231 in long runs),
+  // one sequence of 2K keys 12.4 against 15.5 us; 28 rows (32 columns) 208 against 185 us.
+  if (shape->head_dim == 128 && shape->max_q * p.group <= DecCfg::N)
+    return launch_decode_chunk(shape, p, cap, q, q_stride, k_pool, v_pool, st);
   if (shape->head_dim == 128)
     return L.nt == 1 ? launch_chunk_n<128, 1>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
                      : launch_chunk_n<128, 2>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
@@ -1415,6 +1415,8 @@ cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_pa
   p.tile_tokens = 128 / p.group;
   p.last_q = last_q;
   const int most = last_q > 0 && last_q < shape->max_q ? last_q : shape->max_q;
+  // a chunk's tiles held in shared memory or streamed past the keys: 65 against 78 us for the
+  // last 64 tokens of a 64K prompt, 44 against 59 us for a decode step of eight sequences
   p.held = most <= 2 * p.tile_tokens;
   p.box_tokens = most < p.tile_tokens ? most : p.tile_tokens;
   p.cols = (p.box_tokens * p.group + 15) / 16 * 16;
@@ -1463,7 +1465,8 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   p.sink = evict->sink;
   p.recent = evict->recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // the largest segment's keys, where they fit beside the static histograms
+  // the largest segment's keys held in shared memory, where they fit beside the histograms
+  // (a 32K cache: 22 against 29 us with the masses read again in every pass)
   const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
   dim3 clusters(EVICT_CL, shape->num_kv_heads, shape->batch);
   if (seg <= EVICT_SEG_MAX) {
