@@ -650,10 +650,15 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
           const float m_loc = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * (CAP || BIAS ? 1.f : prm.score.a);
           const bool resc = m_loc > m_ref + C::kRescale;
           if (__any_sync(0xffffffffu, resc)) {
+            // a bias rises towards the row's own position: the base takes that rise in advance
+            // (up to 2^60, which P, l and O have room for), or steep slopes would move it at
+            // every half block
+            const float m_new =
+                BIAS ? m_loc + fminf(fmaxf(slope * (float)(pos - key0 - 63), 0.f), 60.f) : m_loc;
             if (n > 0) {  // O is at rest once the previous half block's product is done
               if (!wait_warp(b_pv(i), (cnt - 1) & 1)) { ok = false; break; }
               tc_fence_after();
-              const float alpha = resc ? ex2_approx(m_ref - m_loc) : 1.f;
+              const float alpha = resc ? ex2_approx(m_ref - m_new) : 1.f;
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
                 uint32_t r[32];
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
               }
               l *= alpha;
             }
-            if (resc) m_ref = m_loc;
+            if (resc) m_ref = m_new;
           }
           // ---- P = 2^(score - m_ref) as bf16 pairs over the first half of the S columns
           const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
