@@ -408,12 +408,6 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ float fmin3f(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
