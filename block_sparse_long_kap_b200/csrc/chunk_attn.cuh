@@ -284,7 +284,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler too
-  if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) return;
+  if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) {
+    // an earlier launch timed out: nothing is run, and the join (which comes all the same) must
+    // not take what the workspace holds for a list
+    if (tid == 0) prm.joins[blockIdx.x].ntok = 0;
+    return;
+  }
   const int G = prm.group, TOK = prm.tile_tokens, P = prm.page_size;
 
   if (tid == 0) {

@@ -501,6 +501,30 @@ def test_pages_outside_the_pool_are_reported_and_never_touched():
         assert len(same) == c.phys - 1
 
 
+@pytest.mark.parametrize("q,D", [(1, 128), (30, 128), (70, 64)])
+def test_after_a_timeout_that_nobody_read_nothing_is_written(q, D):
+    """A launch that finds COSA_ERR_TIMEOUT pending runs nothing, whatever its workspace held: here
+    ones, which as a join list would name row 1 (and lie in range)."""
+    from helpers import shape_of, to_dev
+    from test_gpu_fault import _case
+    wl, x, _, sel = _case()
+    xd, shape = to_dev(x), shape_of(wl, x)
+    order, count = (torch.from_numpy(sel[n]).cuda() for n in ("order", "count"))
+    osk = torch.zeros(wl.batch, wl.num_q_heads, wl.seq_len, 128, dtype=torch.bfloat16, device="cuda")
+    c = Case([(q, 900), (q, 500)], 4, 2, D, 64, seed=83)
+    want = c.attend()
+    ws = torch.ones(C.cosa_chunk_attention_workspace_size(c.shape) // 4, dtype=torch.int32, device="cuda")
+    C.cosa_debug_osk_wait_fault(0, 20_000_000)  # the bounded wait of another call runs out
+    C.cosa_osk_attention(shape, C.OskParams(1e-4), xd["q"], xd["k_pool"], xd["v_pool"], xd["page_table"], order, count, osk)
+    out, lse = c.attend(ws=ws)
+    torch.cuda.synchronize()
+    assert C.cosa_get_status() == 4
+    assert (out == 7).all() and (lse == 7).all()
+    got = c.attend(ws=ws)
+    assert torch.equal(got[0][:2 * q], want[0][:2 * q]) and torch.equal(got[1][:2 * q], want[1][:2 * q])
+    assert C.cosa_get_status() == 0
+
+
 # ---- a run of them together ---------------------------------------------------------------------------
 def test_a_prompt_in_chunks_decoded_and_evicted():
     """A prompt enters in three chunks with rotary positions of three axes, two tokens are decoded, the
