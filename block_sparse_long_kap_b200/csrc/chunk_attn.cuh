@@ -129,6 +129,13 @@ struct ChunkWalk {
   }
 };
 
+// What a row's sum l makes of its O, and its lse.  l = 0: it sees no key.  A NaN among the scores
+// that it sees makes l NaN, and the row with it.
+__device__ __forceinline__ float row_scale(float l) { return l != 0.f ? 1.f / l : 0.f; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
 // ---- plan -----------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
 
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       if (!have || !warp_works) continue;
       tc_fence_after();
       const bool whole = walk.part < 0;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = row_scale(l);
       const long long r_out = (long long)token * prm.num_q_heads + head;
       const long long r_part =
           (long long)(2 * blockIdx.x + (walk.part > 0 ? 1 : 0)) * prm.part_rows + i * 128 + row;
@@ -745,7 +752,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       if (row_valid) {
         if (whole) {
           if (prm.lse)
-            prm.lse[r_out] = l > 0.f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            prm.lse[r_out] = row_lse(m_ref, l);
         } else {
           prm.part_ml[r_part] = make_float2(m_ref, l);
         }
@@ -799,7 +806,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
     }
   };
   auto finish = [&](int row, float m, float l, const float* o) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = row_scale(l);
     const long long out =
         (long long)(jn.y + tok_of(row)) * p.num_q_heads + jn.z * G + (row & 127) % G;
 #pragma unroll
@@ -807,7 +814,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
       *reinterpret_cast<__nv_bfloat162*>(p.out + out * D + lane * EPL + e) =
           __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
     if (p.lse && lane == 0)
-      p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      p.lse[out] = row_lse(m, l);
   };
   if (n <= 3) {
     float2 ml[JOIN_ROWS][3];
@@ -832,7 +839,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
       for (int e = 0; e < EPL; ++e) o[e] = 0.f;
 #pragma unroll
       for (int s = 0; s < 3; ++s)
-        if (ml[k][s].y > 0.f) {  // (a part without keys has no weight, whatever its O holds)
+        if (ml[k][s].y != 0.f) {  // (a part without keys has no weight, whatever its O holds)
           const float w = tc::ex2_approx(ml[k][s].x - m);
           l = fmaf(w, ml[k][s].y, l);
 #pragma unroll
@@ -854,10 +861,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
       const int cnt = min(32, n - s0);
       const float2 ml =
           lane < cnt ? __ldcg(p.part_ml + slot(s0 + lane, row)) : make_float2(-INFINITY, 0.f);
+      if (!__any_sync(0xffffffffu, ml.y != 0.f)) continue;
       const float mx = fmaxf(m, warp_max(ml.x));
-      if (mx == -INFINITY) continue;
       const float back = tc::ex2_approx(m - mx);  // (from -inf: 0)
-      const float w = ml.y > 0.f ? tc::ex2_approx(ml.x - mx) : 0.f;
+      const float w = ml.y != 0.f ? tc::ex2_approx(ml.x - mx) : 0.f;
       float part = w * ml.y;
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
@@ -872,7 +879,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const float ws = __shfl_sync(0xffffffffu, w, min(s + x, 31));
-          if (s + x < cnt && ws > 0.f)
+          if (s + x < cnt && ws != 0.f)
 #pragma unroll
             for (int e = 0; e < EPL; ++e) o[e] = fmaf(ws, v[x][e], o[e]);
         }

@@ -588,10 +588,9 @@ __global__ void __launch_bounds__(256, 1)
           const float4 e4 = *reinterpret_cast<const float4*>(exch + r * 4);
           const float sum = (e4.x + e4.y) + (e4.z + e4.w);
           if (wk.part < 0) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = row_scale(sum);
             prm.out[at * D + row] = __float2bfloat16_rn(__uint_as_float(o[r]) * inv);
-            if (prm.lse && row == r)
-              prm.lse[at] = sum > 0.f ? (m_ref[r] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            if (prm.lse && row == r) prm.lse[at] = row_lse(m_ref[r], sum);
           } else {
             prm.part_o[(slot + r) * D + row] = __uint_as_float(o[r]);
             if (row == r) prm.part_ml[slot + r] = make_float2(m_ref[r], sum);

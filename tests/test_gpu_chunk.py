@@ -171,6 +171,26 @@ def test_logits_far_apart_move_the_exponent_base(opt, q):
     c.check(*c.attend(score), kw)
 
 
+@pytest.mark.parametrize("kv", [120, 900])  # one block: a whole tile; eight: cut between CTAs
+@pytest.mark.parametrize("q,D", [(2, 128), (30, 128), (70, 64), (110, 128)])
+def test_a_nan_key_reaches_the_rows_that_see_it_and_no_others(kv, q, D):
+    c = Case([(q, kv)], 4, 2, D, 64, seed=84)
+    first = np.zeros(c.T, np.int32)
+    first[1::2] = 8  # odd tokens see only later keys
+    c.k_pool[c.table[0, 0], 0, 5, D // 2] = float("nan")  # key 5 of KV head 0
+    c.d["k_pool"].copy_(c.k_pool)
+    out, lse = c.attend(C.ScoreParams(first_key=torch.from_numpy(first).cuda()))
+    o, l, spread = c.oracle(dict(first_key=first))
+    hit = np.isnan(l)[:q]
+    assert hit.sum() == 2 * len(range(0, q, 2))
+    got, gl = _np(out)[:q], _np(lse)[:q]
+    assert np.isnan(gl[hit]).all() and np.isnan(got[hit]).all()
+    tol = (2.0**-8 + 2 * c.ds({})) * spread + 2.0**-8 * np.abs(o)
+    assert (np.abs(got - o[:q])[~hit] <= tol[:q][~hit]).all()
+    assert (np.abs(gl - l[:q])[~hit] <= c.ds({}) + kv * 2.0**-24 + 2.0**-22 * np.abs(l[:q][~hit])).all()
+    assert C.cosa_get_status() == 0
+
+
 def test_strided_queries_and_null_lse():
     c = Case([(3, 50), (17, 200)], 8, 2, seed=1)
     fused = torch.full((c.T, 8 + 4, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
