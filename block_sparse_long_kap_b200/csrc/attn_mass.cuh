@@ -51,7 +51,8 @@ struct MassParams {
 struct MassRows {
   float c[128];    // -lse in log2 units
   int lo[128], hi[128];
-  float slope[128], pos[128];
+  float slope[128], tok[128];  // tok: counted from the first row's, as the keys are
+                               // (a float does not hold every position past 2^24)
 };
 
 template <int D>
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     // one row's constants from global memory
     struct Row {
-      float c, slope, pos;
+      float c, slope, tok;
       int lo, hi;
     };
     auto load_row = [&](int t) {
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(384, 1)
       v.hi = -1;
       v.c = -INFINITY;
       v.slope = 0.f;
-      v.pos = (float)(r.pos0 + i);
+      v.tok = (float)i;
       if (valid) {
         v.c = __ldg(prm.lse + (long long)(r.tok0 + i) * prm.num_q_heads + r.hk * G + row_g);
         token_range(prm.mask, r.tok0 + i, r.pos0 + i, r.seq.kv, r.prefix, v.lo, v.hi);
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(384, 1)
       m->hi[row] = v.hi;
       if (BIAS) {
         m->slope[row] = 1.4426950408889634f * v.slope;
-        m->pos[row] = v.pos;
+        m->tok[row] = v.tok;
       }
     };
     // the keys that every row of a tile sees: [lo, hi]
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(384, 1)
         if (ok && !wait_warp(b_sfull(sbuf), (n >> 1) & 1)) ok = false;
         if (!ok) continue;
         tc_fence_after();
-        const float fkey = (float)key;
+        const float fkey = (float)(key - r.pos0);
         auto add = [&](auto mask_tag, const uint32_t* v, int c0) {  // 16 rows
           constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(384, 1)
                 pack2(c4.z, c4.w));
             if (BIAS) {
               const float4 s4 = *reinterpret_cast<const float4*>(m->slope + c0 + e);
-              const float4 p4 = *reinterpret_cast<const float4*>(m->pos + c0 + e);
+              const float4 p4 = *reinterpret_cast<const float4*>(m->tok + c0 + e);
               x0 = fma2(pack2(-s4.x, -s4.y), pack2(fabsf(fkey - p4.x), fabsf(fkey - p4.y)), x0);
               x1 = fma2(pack2(-s4.z, -s4.w), pack2(fabsf(fkey - p4.z), fabsf(fkey - p4.w)), x1);
             }

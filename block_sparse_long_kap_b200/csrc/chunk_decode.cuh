@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256, 1)
         rlo[row] = lo;
         rhi[row] = hi;
         rsl[row] = slope;
-        rpos[row] = (float)(wk.tile.pos0 + tok);
+        rpos[row] = (float)tok;  // (a float does not hold every position past 2^24)
       }
       named_bar_sync(1, 128);
       // the keys that every row sees: [alo, ahi]
@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(256, 1)
       }
       for (int j = 0; j < wk.nb; ++j, ++cnt) {
         const int buf = cnt & 1, key0 = (wk.jb + j) * C::KB, key = key0 + row;
+        const float ahead = (float)(key - wk.tile.pos0);  // of the first new token
         if (ok && !wait_warp(b_sfull(buf), (cnt >> 1) & 1)) ok = false;
         float x[N], wmax[N];
         bool grow = false;
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int r = r0; r < r0 + 4; ++r) {
               x[r] = score_log2<CAP>(prm.score, __uint_as_float(sc[r]));
-              if (BIAS) x[r] = fmaf(-rsl[r], fabsf((float)key - rpos[r]), x[r]);
+              if (BIAS) x[r] = fmaf(-rsl[r], fabsf(ahead - rpos[r]), x[r]);
               if (!plain && (key < rlo[r] || key > rhi[r])) x[r] = -INFINITY;
               wmax[r] = redux_max(x[r]);
               grow = grow || (r < nrow && wmax[r] > m_ref[r] + C::kRescale);

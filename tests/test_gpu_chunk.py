@@ -191,6 +191,40 @@ def test_a_nan_key_reaches_the_rows_that_see_it_and_no_others(kv, q, D):
     assert C.cosa_get_status() == 0
 
 
+@pytest.mark.parametrize("q,D", [(3, 128), (20, 128), (3, 64), (100, 64)])
+def test_distances_at_positions_past_what_fp32_counts(q, D):
+    """2^24 + 1001 keys (the pages named over and over): a float no longer holds every position, and
+    a bias by distance needs it to one key.  Steep slopes leave the last 2,000 keys to compare."""
+    n, P = 2**24 + 1001, 128
+    c = Case([(q, 1024)], 2, 1, D, P, seed=85)
+    g = torch.Generator().manual_seed(86)
+    table = c.table[0, torch.randint(0, 8, (1, -(-n // P)), generator=g)]
+    c.kv, c.table, c.pps = np.array([n], np.int32), table, table.shape[1]
+    c.shape.max_kv, c.shape.pages_per_seq = n, c.pps
+    c.d["table"], c.d["kv"] = table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda")
+    slopes = np.array([0.5, 0.25], np.float32)
+    score = C.ScoreParams(slopes=torch.from_numpy(slopes).cuda())
+    out, lse = c.attend(score)
+    off = (n - 2048) // P * P
+    args = _np(c.q), _np(c.k_pool)
+    o, l, spread = K.chunk_attention(*args, _np(c.v_pool), table[:, off // P:].numpy(), c.cu, c.kv - off, c.scale,
+                                     slopes=slopes)
+    tol = (2.0**-8 + 2 * c.ds({})) * spread + 2.0**-8 * np.abs(o)
+    assert (np.abs(_np(out) - o)[:q] <= tol[:q]).all()
+    assert (np.abs(_np(lse) - l)[:q] <= c.ds({}) + 2048 * 2.0**-24 + 2.0**-22 * (np.abs(l[:q]) + 2)).all()
+    mass = torch.zeros(1, 1, c.pps * P, device="cuda")
+    C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, score=score)
+    want = K.attention_mass(*args, table[:, off // P:].numpy(), c.cu, c.kv - off, _np(lse),
+                            np.zeros((1, 1, c.pps * P - off)), c.scale, slopes=slopes)
+    got = _np(mass)
+    rel = c.ds({}) + 2.0**-22 * (np.abs(l[:q]).max() + 2) + 2 * q * 2.0**-24
+    # a weight's share of the distance's own rounding: slope x distance x 2^-23 in its exponent
+    far = slopes.max() * (n - off) * 2.0**-23
+    assert (np.abs(got[..., off:] - want) <= (rel + far) * want + 1e-30).all()
+    assert (got[..., :off] < 1e-30).all()
+    assert C.cosa_get_status() == 0
+
+
 def test_strided_queries_and_null_lse():
     c = Case([(3, 50), (17, 200)], 8, 2, seed=1)
     fused = torch.full((c.T, 8 + 4, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
