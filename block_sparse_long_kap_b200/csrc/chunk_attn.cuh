@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const int pos = walk.tile.pos0 + i * TOK + row_tok;
       const bool row_valid = row_tok < min(TOK, ntok);
       const int head = walk.hk * G + row_g;
-      int lo = INT_MIN, hi = INT_MAX;  // rows without a token need no mask: their result goes nowhere
+      int lo = 0, hi = INT_MAX;  // rows without a token need no mask: their result goes nowhere
       float slope = 0.f;
       if (row_valid) {
         token_range(prm.mask, token, pos, walk.tile.kv, walk.tile.prefix, lo, hi);

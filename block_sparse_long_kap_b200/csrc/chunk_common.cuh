@@ -50,7 +50,7 @@ __device__ __forceinline__ void token_range(const ChunkMask& m, int token, int p
                                             int prefix, int& lo, int& hi) {
   lo = m.first_key ? max(__ldg(m.first_key + token), 0) : 0;
   if (m.window > 0) lo = max(lo, pos - m.window + 1);
-  hi = min(max(pos, prefix - 1), kv - 1);
+  hi = min(max(pos, max(prefix, 0) - 1), kv - 1);
 }
 
 // Pairs of floats in one 64-bit register: the FMA pipe takes both in one instruction.

@@ -1442,6 +1442,7 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   if (!k_pool || !v_pool || !page_table || !kv_len || !mass || !dst_table || !kept || !new_len)
     return COSA_ERR_INVALID_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool)) return COSA_ERR_INVALID_ARG;
+  if (mass_out && mass_out == mass) return COSA_ERR_INVALID_ARG;  // strides differ, rows move
   if (evict->budget > (1 << 30)) return COSA_ERR_UNSUPPORTED;
   EvictParams p;
   std::memset(&p, 0, sizeof(p));

@@ -125,6 +125,9 @@ def test_mass_and_evict_checks():
         bad = list(ok)
         bad[i] = None
         assert L.cosa_cache_evict(*bad) == 1, i
+    bad = list(ok)
+    bad[6] = bad[10] = 64  # masses written over the ones being read
+    assert L.cosa_cache_evict(*bad) == 1
     for budget, sink, recent in ((0, 0, 0), (10, -1, 0), (10, 0, -1), (10, 6, 5),
                                  (10, 2**31 - 1, 2**31 - 1)):
         bad = list(ok)

@@ -225,6 +225,27 @@ def test_distances_at_positions_past_what_fp32_counts(q, D):
     assert C.cosa_get_status() == 0
 
 
+@pytest.mark.parametrize("q,D", [(2, 128), (40, 64)])
+def test_extreme_mask_values(q, D):
+    """Lengths of a prefix and first keys at the ends of int32, windows at its top."""
+    c = Case([(q, 300), (q, 300), (q, 300)], 4, 2, D, 64, seed=87)
+    first = np.zeros(c.T, np.int64)
+    first[0::3], first[1::3] = -2**31, 2**31 - 1
+    kw = dict(first_key=first.astype(np.int32), prefix_len=np.array([-2**31, 2**31 - 1, 0], np.int32), window=2**31 - 1)
+    score = C.ScoreParams(window=2**31 - 1, first_key=torch.from_numpy(kw["first_key"]).cuda(),
+                          prefix_len=torch.from_numpy(kw["prefix_len"]).cuda())
+    ref = c.oracle(dict(kw, first_key=np.maximum(first, 0)))
+    out, lse = c.attend(score)
+    c.check(out, lse, {}, ref)
+    mass = torch.zeros(3, 2, c.pps * 64, device="cuda")
+    C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, score=score)
+    want = K.attention_mass(_np(c.q), _np(c.k_pool), c.table.numpy(), c.cu, c.kv, _np(lse), np.zeros(mass.shape), c.scale,
+                            **dict(kw, first_key=np.maximum(first, 0)))
+    rel = c.ds({}) + 2.0**-22 * (np.abs(ref[1][np.isfinite(ref[1])]).max() + 2) + 2 * q * 2.0**-24
+    assert (np.abs(_np(mass) - want) <= rel * want + 1e-30).all()
+    assert C.cosa_get_status() == 0
+
+
 def test_strided_queries_and_null_lse():
     c = Case([(3, 50), (17, 200)], 8, 2, seed=1)
     fused = torch.full((c.T, 8 + 4, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
