@@ -52,7 +52,7 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc_path(), *GENCODE, "-O3", "-lineinfo", "-std=c++17", "--split-compile=0",
+    cmd = [nvcc_path(), *GENCODE, "-O3", "-lineinfo", "-std=c++17",
            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
            "-o", LIB + ".tmp", *sources()]
     if ptxas_v:
