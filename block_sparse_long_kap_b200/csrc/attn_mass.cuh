@@ -18,9 +18,9 @@
 //                        buffers each, so the next tile's product runs under this one's
 //                        exponentials.
 // Bound by the K bytes for a few rows: a decode step of eight sequences of up to 16K keys (218 MB)
-// takes 44 us, 0.76 of a copy's rate, the rest is the start of the stream and the last pair's
+// takes 43 us, 0.78 of a copy's rate, the rest is the start of the stream and the last pair's
 // way through.  For many rows by the exponentials (16 a cycle and SM): the last 64 tokens of 32
-// heads on 64K keys are 134 M of them, 30 us, and take 65 us (special-function unit 50 % busy,
+// heads on 64K keys are 134 M of them, 30 us, and take 62 us (special-function unit 50 % busy,
 // tensor core 25 %); a quarter of them as a polynomial on the FMA pipe gave nothing.
 // A softmax warp whose wait ran out keeps meeting the others at their named barrier, so that
 // none waits there for good.

@@ -31,8 +31,8 @@
 // product (relative error 2^-8 a weight at most, averaged over the keys), its sum is not.
 // Every wait is bounded, as in the dense kernel.
 //
-// Measured: 1,050 TFLOP/s on a 16K prompt (32 / 8 heads, D = 128; the dense kernel the same),
-// and 1.23-1.27 ms for 2,048 tokens on 32K keys in a long run, 0.55-0.57 of the burst rate: the
+// Measured: 1,010-1,090 TFLOP/s on a 16K prompt (32 / 8 heads, D = 128; the dense kernel beside it
+// 930-960), and 1.20 ms for 2,048 tokens on 32K keys in a long run, 0.58 of the burst rate: the
 // power cap holds the clock at 1.65 GHz there.  Moving a quarter of the exponentials to the FMA
 // pipe shortens the softmax and lengthens the run (1.30 -> 1.33 ms): what costs then is energy.
 #pragma once

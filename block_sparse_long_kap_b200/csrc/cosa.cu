@@ -508,8 +508,9 @@ ChunkLayout chunk_layout(const cosa_chunk_t* s) {
   ChunkLayout L;
   const int G = s->num_q_heads / s->num_kv_heads, tok = 128 / G;
   // one tile at a time while a sequence's rows fit in it: the pair's second softmax group would
-  // be idle and a V slot fewer is left.  Measured, one tile against a pair: 20 rows 311 against
-  // 327 us, 64 rows 121 against 124 us (D = 64), 7 rows 184 against 191 us (D = 64)
+  // be idle, a V slot fewer is left and the partial rows take more room.  Measured, one tile
+  // against a pair, D = 64: 7 rows of 32 sequences 189 against 193 us, one sequence of 2K keys 14.7
+  // against 15.2 us; at 20 to 128 rows both are within the runs' spread
   L.nt = s->max_q <= tok ? 1 : 2;
   L.part_rows = L.nt == 2 ? 256 : s->max_q * G;
   const size_t span = (size_t)tok * L.nt;
@@ -1372,8 +1373,8 @@ cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_p
   const bool cap = score && score->softcap > 0.f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Up to 16 rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
-  // 32K keys, transposed against tiled: 7 rows 198 against 202 us (205 against 231 in long runs),
-  // one sequence of 2K keys 12.4 against 15.5 us; 28 rows (32 columns) 208 against 185 us.
+  // 32K keys, transposed against tiled: 7 rows 199 against 208 us (205 against 231 in long runs),
+  // one sequence of 2K keys 11.9 against 17.8 us; 28 rows (32 columns) 208 against 185 us.
   if (shape->head_dim == 128 && shape->max_q * p.group <= DecCfg::N)
     return launch_decode_chunk(shape, p, cap, q, q_stride, k_pool, v_pool, st);
   if (shape->head_dim == 128)
@@ -1415,8 +1416,8 @@ cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_pa
   p.tile_tokens = 128 / p.group;
   p.last_q = last_q;
   const int most = last_q > 0 && last_q < shape->max_q ? last_q : shape->max_q;
-  // a chunk's tiles held in shared memory or streamed past the keys: 65 against 78 us for the
-  // last 64 tokens of a 64K prompt, 44 against 59 us for a decode step of eight sequences
+  // a chunk's tiles held in shared memory or streamed past the keys: 62 against 73 us for the
+  // last 64 tokens of a 64K prompt, 43 against 54 us for a decode step of eight sequences
   p.held = most <= 2 * p.tile_tokens;
   p.box_tokens = most < p.tile_tokens ? most : p.tile_tokens;
   p.cols = (p.box_tokens * p.group + 15) / 16 * 16;
@@ -1467,7 +1468,7 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   p.recent = evict->recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the largest segment's keys held in shared memory, where they fit beside the histograms
-  // (a 32K cache: 22 against 29 us with the masses read again in every pass)
+  // (a 32K cache: 18 against 24 us with the masses read again in every pass)
   const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
   dim3 clusters(EVICT_CL, shape->num_kv_heads, shape->batch);
   if (seg <= EVICT_SEG_MAX) {
