@@ -8,8 +8,8 @@
 // pair serves all heads, so the table of a CTA's tokens is made once in shared memory.
 // The work is the copy: every element is read and written once, 16 bytes a lane.
 //
-// Measured: 32K tokens of 80 heads (1.33 GB) 226-234 us, 0.87-0.90 of a copy's rate; 8,191 tokens of 36
-// heads (151 MB) 32-34 us, where launch, table and tail are a quarter; a decode step of 64
+// Measured: 32K tokens of 80 heads (1.33 GB) 223 us, 0.91 of a copy's rate; 8,191 tokens of 36
+// heads (151 MB) 33 us, where launch, table and tail are a quarter; a decode step of 64
 // sequences 3.3 us, its table and one trip to memory.  Deeper unrolling (2 to 4 units a thread
 // in flight) took 249 to 364 us for the first.
 #pragma once
@@ -70,10 +70,12 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return v;
 }
 
+// Six CTAs an SM (42 registers): 223 us for 32K tokens of 80 heads; with the compiler's 48 and five
+// CTAs 232, with seven or eight 235.
 // grid (token blocks, parts of a token's units); dynamic shared memory: (cos, sin) of
 // tokens_per_cta * half pairs
 template <int D>
-__global__ void __launch_bounds__(CHUNK_WRITE_THREADS) chunk_write_kernel(const ChunkWriteParams p) {
+__global__ void __launch_bounds__(CHUNK_WRITE_THREADS, 6) chunk_write_kernel(const ChunkWriteParams p) {
   constexpr int UPH = D / 16;  // units per head
   constexpr int MAX_TOK = 16;
   extern __shared__ float4 cs[];           // [token][4][half / 8]: pairs 8c + 2q, 8c + 2q + 1
