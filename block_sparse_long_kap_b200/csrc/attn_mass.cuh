@@ -77,7 +77,7 @@ struct MassCfg {
   static_assert(OFF_CUM + (CHUNK_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory budget");
 };
 
-template <int D, bool CAP, bool BIAS>
+template <int D, CapForm CAP, bool BIAS>  // CAP: none, far, each
 __global__ void __launch_bounds__(384, 1)
     attn_mass_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k, const MassParams prm) {
@@ -437,10 +437,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(m->c + c0 + e);
-            f32x2 x0 = score2_log2<CAP, false>(
+            f32x2 x0 = score2_log2<CAP>(
                 prm.score, pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
                 pack2(c4.x, c4.y));
-            f32x2 x1 = score2_log2<CAP, false>(
+            f32x2 x1 = score2_log2<CAP>(
                 prm.score, pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
                 pack2(c4.z, c4.w));
             if (BIAS) {

@@ -260,7 +260,7 @@ struct ChunkCfg {
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 };
 
-template <int D, int NT, bool CAP, bool BIAS>
+template <int D, int NT, CapForm CAP, bool BIAS>  // CAP: none, or the form beyond y = 0.625
 __global__ void __launch_bounds__(128 + 128 * NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -627,11 +627,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
               far = fmax3f(far, fabsf(__uint_as_float(sc[e])), fabsf(__uint_as_float(sc[e + 1])));
-            auto shape = [&](auto small_tag) {
+            auto shape = [&](auto form_tag) {
 #pragma unroll
               for (int e = 0; e < 64; e += 2) {
                 float x0, x1;
-                unpack2(score2_log2<true, decltype(small_tag)::value>(
+                unpack2(score2_log2<decltype(form_tag)::value>(
                             prm.score, pack2(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])),
                             both(0.f)),
                         x0, x1);
@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
                 sc[e + 1] = __float_as_uint(x1);
               }
             };
-            if (__all_sync(0xffffffffu, !row_valid || far <= prm.score.lim)) shape(std::true_type{});
-            else shape(std::false_type{});
+            if (__all_sync(0xffffffffu, !row_valid || far <= prm.score.lim))
+              shape(std::integral_constant<CapForm, CAP_NEAR>{});
+            else
+              shape(std::integral_constant<CapForm, CAP>{});
           }
           if (BIAS) {
             const f32x2 d0 = both((float)(key0 - pos)), mul = both(CAP ? 1.f : prm.score.a);

@@ -135,12 +135,24 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
 __device__ __forceinline__ f32x2 both(float a) { return pack2(a, a); }
 
 // Scores in log2 units from raw products.  Plain: raw * a.  Capped: with y = raw * scale / c,
-//   c tanh(y) = c - 2c / (1 + e^2y),
-// the exponential and the reciprocal on the special-function unit: absolute error about
-// c * 2^-23, where the hardware tanh (relative error 2^-11) would move a logit near a cap of
-// 50 by 0.02.  While |y| <= 0.625 (logits well inside the cap, the usual case) an odd
-// polynomial of degree 9 does (least absolute error on that range, 4.3e-8), on the FMA pipe:
-// two special-function results less an element, of three.
+// by the size of y:
+//   |y| <= 0.625   c (y + y z q(z)), z = y^2: an odd polynomial of degree 9 (least absolute error of
+//                  the tanh on that range, 4.3e-8; of the score 2^-22.1), on the FMA pipe
+//   beyond         c tanh(y) = c - 2c / (1 + e^2y), the exponential and the reciprocal on the
+//                  special-function unit: absolute error about c * 2^-23, a score's own rounding
+//                  here, but for a small score under a large cap all of it (9e-3 at a cap of
+//                  10^5).  (The hardware tanh, relative error 2^-11, would move a logit near a cap
+//                  of 50 by 0.02.)
+// The first form leaves the special-function unit two results an element: the attention's warps take
+// it (CAP_NEAR) where all their scores are in its range, the usual case.  For the others, and for the
+// mass, whose exponent needs no maximum first:
+//   CAP_FAR   the second form for all scores, up to a cap of 64: its error is at most 2^-17 there, two
+//             roundings of a score of 64
+//   CAP_EACH  larger caps: chosen for each score.  (For all caps it took 276 against 242 us on packed
+//             documents, 149 against 121 us for the mass of 64 tokens on 64K keys, both with scores
+//             beyond their cap of 2.)
+enum CapForm { CAP_NONE, CAP_NEAR, CAP_FAR, CAP_EACH };
+constexpr float kCapFarMax = 64.f;
 struct ScoreShape {
   float a;    // scale * log2 e
   float e2;   // capped: 2 * scale / c * log2 e
@@ -155,29 +167,27 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-template <bool CAP>
-__device__ __forceinline__ float score_log2(const ScoreShape& s, float raw) {
-  if (!CAP) return raw * s.a;
-  const float r = rcp_approx(1.f + tc::ex2_approx(raw * s.e2));
-  return fmaf(-2.f * s.cap, r, s.cap);
+__device__ __forceinline__ float cap_far(const ScoreShape& s, float raw) {
+  return fmaf(-2.f * s.cap, rcp_approx(1.f + tc::ex2_approx(raw * s.e2)), s.cap);
 }
 
-// A pair of scores in log2 units plus `add`; SMALL: both products are within s.lim.
-template <bool CAP, bool SMALL>
+// A pair of scores in log2 units plus `add`; CAP_NEAR: both products are within s.lim.
+template <CapForm FORM>
 __device__ __forceinline__ f32x2 score2_log2(const ScoreShape& s, f32x2 raw, f32x2 add) {
-  if (!CAP) return fma2(raw, both(s.a), add);
-  if (SMALL) {  // y + y z q(z), z = y^2, scaled by c log2 e
-    const f32x2 y = mul2(raw, both(s.y)), z = mul2(y, y);
-    f32x2 q = fma2(z, both(0.0148892366f), both(-0.0517016767f));
-    q = fma2(q, z, both(0.133020084f));
-    q = fma2(q, z, both(-0.333318751f));
-    return fma2(mul2(raw, both(s.a)), mul2(q, z), fma2(raw, both(s.a), add));
-  }
+  if (FORM == CAP_NONE) return fma2(raw, both(s.a), add);
   float r0, r1;
   unpack2(raw, r0, r1);
-  return add2(pack2(score_log2<true>(s, r0), score_log2<true>(s, r1)), add);
+  if (FORM == CAP_FAR) return add2(pack2(cap_far(s, r0), cap_far(s, r1)), add);
+  const f32x2 y = mul2(raw, both(s.y)), z = mul2(y, y);
+  f32x2 q = fma2(z, both(0.0148892366f), both(-0.0517016767f));
+  q = fma2(q, z, both(0.133020084f));
+  q = fma2(q, z, both(-0.333318751f));
+  const f32x2 x = mul2(raw, both(s.a)), qz = mul2(q, z);
+  if (FORM == CAP_NEAR) return fma2(x, qz, fma2(raw, both(s.a), add));
+  float x0, x1;
+  unpack2(fma2(x, qz, x), x0, x1);
+  return add2(pack2(fabsf(r0) <= s.lim ? x0 : cap_far(s, r0), fabsf(r1) <= s.lim ? x1 : cap_far(s, r1)), add);
 }
-
 // The waiting itself, kept out of line: two dozen inlined copies of these loops would not
 // leave the instruction cache room for the loops that work.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at,

@@ -488,8 +488,13 @@ __global__ void __launch_bounds__(256, 1)
           for (int r0 = 0; r0 < N; r0 += 4) {
             if (r0 >= nrow) break;  // one jump past all the code of rows that do not exist
 #pragma unroll
+            for (int r = r0; r < r0 + 4; r += 2)
+              unpack2(score2_log2<CAP ? CAP_EACH : CAP_NONE>(
+                          prm.score, pack2(__uint_as_float(sc[r]), __uint_as_float(sc[r + 1])),
+                          both(0.f)),
+                      x[r], x[r + 1]);
+#pragma unroll
             for (int r = r0; r < r0 + 4; ++r) {
-              x[r] = score_log2<CAP>(prm.score, __uint_as_float(sc[r]));
               if (BIAS) x[r] = fmaf(-rsl[r], fabsf(ahead - rpos[r]), x[r]);
               if (!plain && (key < rlo[r] || key > rhi[r])) x[r] = -INFINITY;
               wmax[r] = redux_max(x[r]);

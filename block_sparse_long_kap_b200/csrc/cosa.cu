@@ -2,6 +2,7 @@
 // kernel launches.  All arithmetic of the method runs in the kernels included
 // below; this file only checks sizes and marshals pointers.
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -445,7 +446,8 @@ cosa_status_t check_chunk(const cosa_chunk_t* s) {
 
 cosa_status_t check_score(const cosa_score_params_t* s) {
   if (!s) return COSA_OK;
-  if (!(s->softcap >= 0.f) || !std::isfinite(s->softcap) || s->window < 0)
+  // (2^126: twice the cap in log2 units is still finite)
+  if (!(s->softcap >= 0.f) || !(s->softcap < 8.507059e37f) || s->window < 0)
     return COSA_ERR_INVALID_ARG;
   return COSA_OK;
 }
@@ -468,16 +470,23 @@ ChunkMask chunk_mask(const cosa_score_params_t* s) {
 
 ScoreShape score_shape(const cosa_chunk_t* s, const cosa_score_params_t* sc) {
   const double log2e = 1.4426950408889634, scale = s->softmax_scale;
+  // (finite: under the smallest caps a product of zero stays zero)
+  auto fin = [](double x) { return x < FLT_MAX ? (float)x : FLT_MAX; };
   ScoreShape r;
   std::memset(&r, 0, sizeof(r));
-  r.a = (float)(scale * log2e);
+  r.a = fin(scale * log2e);
   if (sc && sc->softcap > 0.f) {
-    r.e2 = (float)(2.0 * scale / sc->softcap * log2e);
-    r.cap = (float)(sc->softcap * log2e);
-    r.y = (float)(scale / sc->softcap);
-    r.lim = (float)(0.625 * sc->softcap / scale);
+    r.e2 = fin(2.0 * scale / sc->softcap * log2e);
+    r.cap = fin(sc->softcap * log2e);
+    r.y = fin(scale / sc->softcap);
+    r.lim = fin(0.625 * sc->softcap / scale);
   }
   return r;
+}
+
+CapForm cap_form(const cosa_score_params_t* sc) {
+  if (!sc || !(sc->softcap > 0.f)) return CAP_NONE;
+  return sc->softcap <= kCapFarMax ? CAP_FAR : CAP_EACH;
 }
 
 // bf16 [tokens][heads][D] with a token stride: box = 64 columns x G heads x `tokens` tokens
@@ -589,7 +598,7 @@ cosa_status_t launch_join(const ChunkAttnParams& prm, cudaStream_t st) {
                     0, st, prm);
 }
 
-template <int D, int NT, bool CAP, bool BIAS>
+template <int D, int NT, CapForm CAP, bool BIAS>
 cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, const void* q,
                              int64_t q_stride, const void* k_pool, const void* v_pool,
                              cudaStream_t st) {
@@ -609,6 +618,17 @@ cosa_status_t launch_chunk_t(const cosa_chunk_t* s, const ChunkAttnParams& prm, 
   e = launch_pdl(kern, dim3(NUM_SMS), Cfg::THREADS, Cfg::SMEM_ALLOC, st, mq, mk, mv, prm);
   if (e != COSA_OK) return e;
   return launch_join<D>(prm, st);
+}
+
+// go(form, bias) for the cap's form and whether slopes are given
+template <typename Go>
+cosa_status_t with_form(CapForm cap, const float* slopes, const Go& go) {
+  auto with_bias = [&](auto form) {
+    return slopes ? go(form, std::true_type{}) : go(form, std::false_type{});
+  };
+  if (cap == CAP_FAR) return with_bias(std::integral_constant<CapForm, CAP_FAR>{});
+  if (cap == CAP_EACH) return with_bias(std::integral_constant<CapForm, CAP_EACH>{});
+  return with_bias(std::integral_constant<CapForm, CAP_NONE>{});
 }
 
 template <bool CAP, bool BIAS>
@@ -641,17 +661,16 @@ cosa_status_t launch_decode_chunk(const cosa_chunk_t* s, const ChunkAttnParams& 
 }
 
 template <int D, int NT>
-cosa_status_t launch_chunk_n(const cosa_chunk_t* s, const ChunkAttnParams& prm, bool cap,
+cosa_status_t launch_chunk_n(const cosa_chunk_t* s, const ChunkAttnParams& prm, CapForm cap,
                              const void* q, int64_t q_stride, const void* k_pool,
                              const void* v_pool, cudaStream_t st) {
-  const bool bias = prm.slopes != nullptr;
-  if (cap && bias) return launch_chunk_t<D, NT, true, true>(s, prm, q, q_stride, k_pool, v_pool, st);
-  if (cap) return launch_chunk_t<D, NT, true, false>(s, prm, q, q_stride, k_pool, v_pool, st);
-  if (bias) return launch_chunk_t<D, NT, false, true>(s, prm, q, q_stride, k_pool, v_pool, st);
-  return launch_chunk_t<D, NT, false, false>(s, prm, q, q_stride, k_pool, v_pool, st);
+  auto go = [&](auto form, auto bias) {
+    return launch_chunk_t<D, NT, decltype(form)::value, decltype(bias)::value>(s, prm, q, q_stride, k_pool, v_pool, st);
+  };
+  return with_form(cap, prm.slopes, go);
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, CapForm CAP, bool BIAS>
 cosa_status_t launch_mass_t(const cosa_chunk_t* s, const MassParams& prm, const void* q,
                             int64_t q_stride, const void* k_pool, cudaStream_t st) {
   using Cfg = MassCfg<D>;
@@ -668,13 +687,12 @@ cosa_status_t launch_mass_t(const cosa_chunk_t* s, const MassParams& prm, const 
 }
 
 template <int D>
-cosa_status_t launch_mass_d(const cosa_chunk_t* s, const MassParams& prm, bool cap, const void* q,
+cosa_status_t launch_mass_d(const cosa_chunk_t* s, const MassParams& prm, CapForm cap, const void* q,
                             int64_t q_stride, const void* k_pool, cudaStream_t st) {
-  const bool bias = prm.slopes != nullptr;
-  if (cap && bias) return launch_mass_t<D, true, true>(s, prm, q, q_stride, k_pool, st);
-  if (cap) return launch_mass_t<D, true, false>(s, prm, q, q_stride, k_pool, st);
-  if (bias) return launch_mass_t<D, false, true>(s, prm, q, q_stride, k_pool, st);
-  return launch_mass_t<D, false, false>(s, prm, q, q_stride, k_pool, st);
+  auto go = [&](auto form, auto bias) {
+    return launch_mass_t<D, decltype(form)::value, decltype(bias)::value>(s, prm, q, q_stride, k_pool, st);
+  };
+  return with_form(cap, prm.slopes, go);
 }
 
 // Test hook of cosa_debug_osk_wait_fault: one-shot, per host thread.
@@ -1370,13 +1388,13 @@ cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_p
   p.max_tiles = L.max_tiles;
   p.score = score_shape(shape, score);
   p.timeout_ns = kWaitTimeoutNs;
-  const bool cap = score && score->softcap > 0.f;
+  const CapForm cap = cap_form(score);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Up to 16 rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
   // 32K keys, transposed against tiled: 7 rows 199 against 208 us (205 against 231 in long runs),
   // one sequence of 2K keys 11.9 against 17.8 us; 28 rows (32 columns) 208 against 185 us.
   if (shape->head_dim == 128 && shape->max_q * p.group <= DecCfg::N)
-    return launch_decode_chunk(shape, p, cap, q, q_stride, k_pool, v_pool, st);
+    return launch_decode_chunk(shape, p, cap != CAP_NONE, q, q_stride, k_pool, v_pool, st);
   if (shape->head_dim == 128)
     return L.nt == 1 ? launch_chunk_n<128, 1>(shape, p, cap, q, q_stride, k_pool, v_pool, st)
                      : launch_chunk_n<128, 2>(shape, p, cap, q, q_stride, k_pool, v_pool, st);
@@ -1424,7 +1442,7 @@ cosa_status_t cosa_attention_mass(const cosa_chunk_t* shape, const cosa_score_pa
   p.decay = decay;
   p.score = score_shape(shape, score);
   p.timeout_ns = kWaitTimeoutNs;
-  const bool cap = score && score->softcap > 0.f;
+  const CapForm cap = cap_form(score);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return shape->head_dim == 128 ? launch_mass_d<128>(shape, p, cap, q, q_stride, k_pool, st)
                                 : launch_mass_d<64>(shape, p, cap, q, q_stride, k_pool, st);

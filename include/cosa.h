@@ -443,7 +443,8 @@ typedef struct {
 
 /* How scores are shaped and which keys a token sees.  NULL means plain causal. */
 typedef struct {
-  float softcap;             /* c > 0: s <- c * tanh(s / c) on the scaled score; 0: off  */
+  float softcap;             /* 0 < c < 2^126: s <- c * tanh(s / c) on the scaled score;
+                                0: off                                                   */
   int32_t window;            /* w > 0: keys older than t - w + 1 are not seen; 0: off    */
   const float* slopes;       /* fp32 [H_q] or NULL: s <- s - slopes[h] * |t - key| (after
                                 the cap): a bias that depends on distance                */

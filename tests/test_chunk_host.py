@@ -155,3 +155,12 @@ def test_binding_refuses_host_tensors_shapes_and_types(monkeypatch):
         C.cosa_attention_mass(s, None, pool, pt, cu, kv, ws, ws)
     with pytest.raises(ValueError, match="4 rotary axes"):
         C.RopeParams(sections=(8, 8, 8, 8, 8)).c()
+
+
+@pytest.mark.parametrize("cap", [8.6e37, 3.4e38])
+def test_caps_past_what_fp32_can_double_are_refused(cap):
+    L, s, ws = C.lib(), C.ChunkShape(**GOOD).c(), _size()[1]
+    p = C._Score(cap, 0, None, None, None)
+    ref, sc = ctypes.byref(s), ctypes.byref(p)
+    assert L.cosa_chunk_attention(ref, sc, 16, 1024, 16, 16, 16, 16, 16, 16, None, 256, ws, None) == 1
+    assert L.cosa_attention_mass(ref, sc, 16, 1024, 16, 16, 16, 16, 16, 0, 1.0, 16, None) == 1

@@ -1,0 +1,97 @@
+"""GPU parity of the chunk operators at the edges of what a call may say.
+
+Tolerances as in test_gpu_chunk.py, but for a capped score, whose error is taken relative to the
+score: the polynomial is off by 2^-22.1 of it at most, the exponential's form (used from
+|y| = 0.625 on, where tanh y > 0.55) by 2^-21.5, with six fp32 roundings of 2^-24 each at most beside
+them: together under 2^-20 |s|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_kap_b200 as C
+from oracle import chunk_oracle as K
+from test_gpu_chunk import Case, _np
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_rows(c, out, lse, kw, ds):
+    o, l, spread = c.oracle(kw)
+    n = int(c.cu[-1])
+    tol = (2.0**-8 + 2 * ds) * spread + 2.0**-8 * np.abs(o)
+    assert (np.abs(_np(out) - o)[:n] <= tol[:n]).all()
+    assert (np.abs(_np(lse) - l)[:n] <= ds + int(c.kv.max()) * 2.0**-24 + 2.0**-22 * np.abs(l[:n])).all()
+
+
+def _check_mass(c, score, kw, lse, ds):
+    mass = torch.zeros(len(c.lens), c.hk, c.pps * c.P, device="cuda")
+    C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, score=score)
+    want = K.attention_mass(_np(c.q), _np(c.k_pool), c.table.numpy(), c.cu, c.kv, _np(lse), np.zeros(mass.shape), c.scale, **kw)
+    n = int(c.cu[-1])
+    rel = ds + 2.0**-22 * (np.abs(_np(lse)[:n]).max() + 2) + (c.shape.max_q * c.hq // c.hk) * 2.0**-24
+    assert (np.abs(_np(mass) - want) <= rel * want + 1e-30).all()
+
+
+# ---- a cap far above the scores -----------------------------------------------------------------------
+FORMS = [(2, 128), (8, 128), (30, 128), (110, 128), (3, 64), (70, 64)]  # transposed, one tile, a pair of tiles
+
+
+@pytest.mark.parametrize("q,D", FORMS)
+@pytest.mark.parametrize("cap", [1e4, 1e6, 1e8, 1e30, 8.5e37])
+def test_a_cap_far_above_the_scores_leaves_them(q, D, cap):
+    c = Case([(q, 700), (q, 130)], 4, 2, D, 64, seed=100)
+    kw = dict(softcap=cap)
+    score = C.ScoreParams(softcap=cap)
+    raw = c.ds({}) / (D * 2.0**-24)  # scale max|q| . max|k|: no score is larger
+    ds = c.ds({}) + 2.0**-20 * raw
+    out, lse = c.attend(score)
+    _check_rows(c, out, lse, kw, ds)
+    _check_mass(c, score, kw, lse, ds)
+    assert C.cosa_get_status() == 0
+
+
+@pytest.mark.parametrize("q,D", FORMS)
+@pytest.mark.parametrize("cap", [1e-44, 1e-38])
+def test_a_cap_of_nothing_makes_every_score_zero(q, D, cap):
+    c = Case([(q, 700), (q, 130)], 4, 2, D, 64, seed=105)
+    kw, score = dict(softcap=cap), C.ScoreParams(softcap=cap)
+    out, lse = c.attend(score)
+    _check_rows(c, out, lse, kw, 2.0**-20)
+    _check_mass(c, score, kw, lse, 2.0**-20)
+
+
+@pytest.mark.parametrize("opt", ["plain", "bias"])
+@pytest.mark.parametrize("q,D", FORMS)
+def test_one_score_at_the_cap_leaves_the_small_ones_beside_it(q, D, opt):
+    """Key 5 of every sequence lies 10^5 below the others and at the cap: it weighs nothing, and
+    what is worked out for it must not cost the others their precision."""
+    c = Case([(q, 700), (q, 130)], 4, 2, D, 64, seed=101)
+    c.q[:, :, 0] = 1.0
+    raw = c.ds({}) / (D * 2.0**-24)
+    ds = c.ds({}) + 2.0**-20 * raw
+    for b in range(2):
+        c.k_pool[c.table[b, 0], :, 5] = 0
+        c.k_pool[c.table[b, 0], :, 5, 0] = -(2.0**20)
+    c.d["q"].copy_(c.q)
+    c.d["k_pool"].copy_(c.k_pool)
+    kw = dict(softcap=1e5)
+    if opt == "bias":
+        kw["slopes"] = np.float32(2.0) ** -np.linspace(5, 9, 4).astype(np.float32)
+        ds += 700 * 2.0**-5 * 2.0**-22  # the bias, rounded twice
+    score = C.ScoreParams(softcap=1e5, slopes=torch.from_numpy(kw["slopes"]).cuda() if "slopes" in kw else None)
+    out, lse = c.attend(score)
+    _check_rows(c, out, lse, kw, ds)
+    _check_mass(c, score, kw, lse, ds)
+    assert C.cosa_get_status() == 0
+
+
+@pytest.mark.parametrize("cap", [20.0, 1e5])
+def test_mass_of_many_tiles_under_a_cap(cap):
+    """A chunk past two tiles: the streamed form."""
+    c = Case([(200, 400)], 8, 2, 128, 64, seed=102)
+    kw, score = dict(softcap=cap), C.ScoreParams(softcap=cap)
+    ds = c.ds({}) + 2.0**-20 * c.ds({}) / (128 * 2.0**-24)
+    out, lse = c.attend(score)
+    _check_rows(c, out, lse, kw, ds)
+    _check_mass(c, score, kw, lse, ds)
