@@ -188,6 +188,7 @@ __device__ __forceinline__ f32x2 score2_log2(const ScoreShape& s, f32x2 raw, f32
   unpack2(fma2(x, qz, x), x0, x1);
   return add2(pack2(fabsf(r0) <= s.lim ? x0 : cap_far(s, r0), fabsf(r1) <= s.lim ? x1 : cap_far(s, r1)), add);
 }
+
 // The waiting itself, kept out of line: two dozen inlined copies of these loops would not
 // leave the instruction cache room for the loops that work.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at,

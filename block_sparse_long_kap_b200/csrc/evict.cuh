@@ -298,27 +298,31 @@ __global__ void __launch_bounds__(GATHER_THREADS) evict_gather_kernel(const Evic
 #pragma unroll
   for (int e = 0; e < GATHER_UNROLL; ++e) {
     const int j = r0 + e * RPB;
-    from[e] = -1;
+    from[e] = to[e] = -1;
     if (src[e] < 0 || src[e] >= p.max_kv) continue;
     const int ps = __ldg(p.page_table + (long long)b * p.pages_per_seq + src[e] / p.page_size);
     const int pd = __ldg(p.dst_table + (long long)b * p.dst_pages + j / p.page_size);
-    if (ps < 0 || ps >= p.num_phys_pages || pd < 0 || pd >= p.num_phys_pages) {
-      if (l == 0) set_status(COSA_ERR_INVALID_ARG);
-      continue;
-    }
-    from[e] = (((long long)ps * p.num_kv_heads + hk) * p.page_size + src[e] % p.page_size) * LPR + l;
+    const bool from_ok = ps >= 0 && ps < p.num_phys_pages, to_ok = pd >= 0 && pd < p.num_phys_pages;
+    if (!(from_ok && to_ok) && l == 0) set_status(COSA_ERR_INVALID_ARG);
+    if (!to_ok) continue;
     to[e] = (((long long)pd * p.num_kv_heads + hk) * p.page_size + j % p.page_size) * LPR + l;
+    if (from_ok)
+      from[e] = (((long long)ps * p.num_kv_heads + hk) * p.page_size + src[e] % p.page_size) * LPR + l;
   }
+  // a key of a page outside the pool reads as zeros, here as in the attention: its slot must not
+  // keep what the new page held
   uint4 k[GATHER_UNROLL], v[GATHER_UNROLL];
 #pragma unroll
-  for (int e = 0; e < GATHER_UNROLL; ++e)
+  for (int e = 0; e < GATHER_UNROLL; ++e) {
+    k[e] = v[e] = make_uint4(0u, 0u, 0u, 0u);
     if (from[e] >= 0) {
       k[e] = reinterpret_cast<const uint4*>(p.k_pool)[from[e]];
       v[e] = reinterpret_cast<const uint4*>(p.v_pool)[from[e]];
     }
+  }
 #pragma unroll
   for (int e = 0; e < GATHER_UNROLL; ++e)
-    if (from[e] >= 0) {
+    if (to[e] >= 0) {
       reinterpret_cast<uint4*>(p.k_pool)[to[e]] = k[e];
       reinterpret_cast<uint4*>(p.v_pool)[to[e]] = v[e];
     }

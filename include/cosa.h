@@ -519,6 +519,8 @@ typedef struct {
  * and no other sequence of the call is given; the old pages stay as they were, so pages
  * shared with other sequences are safe).  mass_out fp32 [B][H_kv][ceil(budget / P) * P]
  * (may be NULL, not mass itself) gets the kept keys' masses, new_len int32 [B] (may be kv_len itself) n'.
+ * A kept key whose page is outside the pool arrives as zeros; nothing is written for a dst_table
+ * entry outside it (both are recorded, as above).
  * mass as for cosa_attention_mass.  shape's num_q_heads, total_q and max_q play no part
  * beyond their checks; a kv_len outside [0, max_kv] is recorded as COSA_ERR_INVALID_ARG in
  * the status word and the sequence left out. */

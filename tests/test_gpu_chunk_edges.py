@@ -95,3 +95,42 @@ def test_mass_of_many_tiles_under_a_cap(cap):
     out, lse = c.attend(score)
     _check_rows(c, out, lse, kw, ds)
     _check_mass(c, score, kw, lse, ds)
+
+
+# ---- eviction from a page outside the pool ----------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [-1, 2**31 - 1, None])
+def test_kept_keys_of_a_bad_page_arrive_as_zeros(D, bad):
+    """A page-table entry outside the pool reads as zeros: before an eviction and after it."""
+    P, budget = 64, 150
+    c = Case([(1, 200), (1, 170)], 4, 2, D, P, seed=103, extra_pages=0)
+    need = -(-budget // P)
+    fresh = torch.full((2 * need, 2, P, D), float("nan"), dtype=torch.bfloat16)
+    kp, vp = (torch.cat([x, fresh]).cuda() for x in (c.k_pool, c.v_pool))
+    c.shape.num_phys_pages = c.phys + 2 * need
+    table = c.table.clone()
+    table[0, 1] = c.shape.num_phys_pages if bad is None else bad
+    dst = torch.arange(2 * need, dtype=torch.int32).view(2, need) + c.phys
+    mass = torch.rand(2, 2, c.pps * P, generator=c.g)
+    kept = torch.empty(2, 2, budget, dtype=torch.int32, device="cuda")
+    n = torch.empty(2, dtype=torch.int32, device="cuda")
+    mo = torch.full((2, 2, need * P), 7.0, device="cuda")
+    before = kp.clone(), vp.clone()
+    C.cosa_cache_evict(c.shape, C.EvictParams(budget, 4, 16), kp, vp, table.cuda(), c.d["kv"], mass.cuda(), dst.cuda(), kept, n,
+                       mass_out=mo)
+    torch.cuda.synchronize()
+    assert C.cosa_get_status() == 1
+    # the same with that page there, and zero
+    k2, v2 = (np.nan_to_num(_np(x)) for x in before)
+    k2[c.table[0, 1]] = v2[c.table[0, 1]] = 0
+    wk, wn, k2, v2, wm = K.cache_evict(k2, v2, c.table.numpy(), c.kv, mass.numpy(), dst.numpy(), budget, 4, 16)
+    assert np.array_equal(_np(kept), wk) and np.array_equal(_np(n), wn)
+    for b in range(2):
+        j = np.arange(budget)
+        page, slot = dst[b].numpy()[j // P], j % P
+        for got, want in ((kp, k2), (vp, v2)):
+            assert np.array_equal(_np(got)[page, :, slot], want[page, :, slot])
+        for h in range(2):
+            assert np.array_equal(_np(mo)[b, h, :budget], wm[b, h].astype(np.float64))
+    for got, was in ((kp, before[0]), (vp, before[1])):  # the old pages are as they were
+        assert np.array_equal(_np(got)[:c.phys], _np(was)[:c.phys], equal_nan=True)
