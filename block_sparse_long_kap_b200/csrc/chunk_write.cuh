@@ -70,12 +70,76 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return v;
 }
 
+// What the kernel below does not find where cu_q goes back: there its count of ends is no guide to a
+// token's sequence, and a token may have several.  A CTA of its own looks every sequence's lengths
+// over, and in that case writes the rows of a token's other sequences, or of all of them where the
+// counted one is not its own.  (Such a cu_q is an error and recorded as one; the sequences that are
+// sound have to come out whole, not fast.)  q is written with a token's first sequence only: in
+// place, a second turn would count.
+__device__ __forceinline__ void chunk_write_review(const ChunkWriteParams& p, int D) {
+  const int tid = threadIdx.x, hq = p.num_q_heads, hk = p.num_kv_heads;
+  bool back = false;
+  for (int b = tid; b < p.seqs.batch; b += CHUNK_WRITE_THREADS) {
+    chunk_seq(p.seqs, b);
+    back |= __ldg(p.seqs.cu_q + b + 1) < __ldg(p.seqs.cu_q + b);
+  }
+  if (!__syncthreads_or(back)) return;
+  for (int t = 0; t < p.seqs.total_q; ++t) {
+    int counted = 0;
+    for (int b = 0; b < p.seqs.batch; ++b) counted += __ldg(p.seqs.cu_q + b + 1) <= t;
+    auto owns = [&](int b, ChunkSeq& s) {
+      s = chunk_seq(p.seqs, b);
+      return s.ok && t >= s.q0 && t < s.q0 + s.q_len;
+    };
+    ChunkSeq s;
+    bool with_q = counted >= p.seqs.batch || !owns(counted, s);
+    for (int b = 0; b < p.seqs.batch; ++b) {
+      if (b == counted || !owns(b, s)) continue;
+      const int pos = s.kv - s.q_len + (t - s.q0);
+      const int phys = __ldg(p.page_table + (long long)b * p.pages_per_seq + pos / p.page_size);
+      const bool page = phys >= 0 && phys < p.num_phys_pages;
+      if (!page) set_status(COSA_ERR_INVALID_ARG);
+      const long long row = (long long)phys * hk * p.page_size + pos % p.page_size;
+      // a thread's item: two elements of a head, a pair that turns together or two that stay
+      for (int x = tid; x < (hq + 2 * hk) * (D / 2); x += CHUNK_WRITE_THREADS) {
+        const int h = x / (D / 2), j = x % (D / 2), g = h < hq ? h : (h - hq) % hk;
+        const bool is_v = h >= hq + hk;
+        if (h < hq ? !with_q : !page) continue;
+        const __nv_bfloat16* src = h < hq ? p.q_tok + t * p.q_tok_stride
+                                          : (is_v ? p.v_tok + t * p.v_tok_stride : p.k_tok + t * p.k_tok_stride);
+        __nv_bfloat16* dst = h < hq ? p.q + t * p.q_stride + g * D
+                                    : (is_v ? p.v_pool : p.k_pool) + (row + (long long)g * p.page_size) * D;
+        src += g * D;
+        const bool halves = j < p.half && !p.adjacent;
+        const int e0 = halves ? j : 2 * j, e1 = halves ? j + p.half : 2 * j + 1;
+        const __nv_bfloat16 x0 = src[e0], x1 = src[e1];
+        if (is_v || j >= p.half) {
+          dst[e0] = x0;
+          dst[e1] = x1;
+          continue;
+        }
+        // (not shared with the kernel below: in a common function it cost that a spilled register, and
+        // 1 % of the time of 32K tokens)
+        const int at = __ldg(p.positions + (long long)rope_axis(p, j) * p.seqs.total_q + t);
+        const double w = (double)at * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
+        float sn, co;
+        sincospif(2.f * (float)(w - rint(w)), &sn, &co);
+        const float a = __bfloat162float(x0), c = __bfloat162float(x1);
+        dst[e0] = __float2bfloat16_rn(a * co - c * sn);
+        dst[e1] = __float2bfloat16_rn(c * co + a * sn);
+      }
+      with_q = false;
+    }
+  }
+}
+
 // Six CTAs an SM (42 registers): 223 us for 32K tokens of 80 heads; with the compiler's 48 and five
 // CTAs 232, with seven or eight 235.
-// grid (token blocks, parts of a token's units); dynamic shared memory: (cos, sin) of
+// grid (token blocks and one CTA more, parts of a token's units); dynamic shared memory: (cos, sin) of
 // tokens_per_cta * half pairs
 template <int D>
-__global__ void __launch_bounds__(CHUNK_WRITE_THREADS, 6) chunk_write_kernel(const ChunkWriteParams p) {
+__global__ void __launch_bounds__(CHUNK_WRITE_THREADS, 6)
+    chunk_write_kernel(const ChunkWriteParams p) {
   constexpr int UPH = D / 16;  // units per head
   constexpr int MAX_TOK = 16;
   extern __shared__ float4 cs[];           // [token][4][half / 8]: pairs 8c + 2q, 8c + 2q + 1
@@ -84,8 +148,10 @@ __global__ void __launch_bounds__(CHUNK_WRITE_THREADS, 6) chunk_write_kernel(con
   const int tok0 = blockIdx.x * p.tokens_per_cta;
   const int n = min(p.tokens_per_cta, p.seqs.total_q - tok0);
   const int half = p.half;
-  if (blockIdx.x == 0 && blockIdx.y == 0)  // every sequence's lengths are looked at once
-    for (int b = tid; b < p.seqs.batch; b += CHUNK_WRITE_THREADS) chunk_seq(p.seqs, b);
+  if (n <= 0) {  // the CTA past the last token
+    if (blockIdx.y == 0) chunk_write_review(p, D);
+    return;
+  }
   // the sequence of token t: the number of sequences that end at or before it
   for (int i = warp; i < n; i += CHUNK_WRITE_THREADS / 32) {
     const int t = tok0 + i;

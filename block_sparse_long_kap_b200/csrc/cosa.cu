@@ -1330,7 +1330,7 @@ cosa_status_t cosa_chunk_write(const cosa_chunk_t* shape, const cosa_rope_params
   if (parts > 65535) return COSA_ERR_UNSUPPORTED;
   const size_t smem = (size_t)p.tokens_per_cta * p.half * 8;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  dim3 grid(blocks, (unsigned)parts);
+  dim3 grid(blocks + 1, (unsigned)parts);
   if (D == 128) chunk_write_kernel<128><<<grid, CHUNK_WRITE_THREADS, smem, st>>>(p);
   else chunk_write_kernel<64><<<grid, CHUNK_WRITE_THREADS, smem, st>>>(p);
   return last_launch();

@@ -406,7 +406,9 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * projection's output: at least H * D, a multiple of 8, heads contiguous.
  * Lengths are checked on the device: a sequence with cu_q decreasing or past total_q,
  * q_len > max_q, kv_len > max_kv or q_len > kv_len is recorded as COSA_ERR_INVALID_ARG in
- * the status word and left out (its outputs keep what they held).  A page-table entry
+ * the status word and left out (its outputs keep what they held); the others are served in full.
+ * (Where cu_q goes back, two of them may own a row: cosa_chunk_write writes it to both caches,
+ * cosa_chunk_attention leaves the result of either in it.)  A page-table entry
  * outside the pool is recorded the same way; its keys read as zeros and nothing is
  * written there.  Keys are addressed by cache position: after an eviction, positions
  * (and the window and distances below) count the kept keys, while the rotation of

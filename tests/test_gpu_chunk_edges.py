@@ -134,3 +134,41 @@ def test_kept_keys_of_a_bad_page_arrive_as_zeros(D, bad):
             assert np.array_equal(_np(mo)[b, h, :budget], wm[b, h].astype(np.float64))
     for got, was in ((kp, before[0]), (vp, before[1])):  # the old pages are as they were
         assert np.array_equal(_np(got)[:c.phys], _np(was)[:c.phys], equal_nan=True)
+
+
+# ---- lengths that go back ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("cu,lens", [
+    ([0, 3, 2, 5], [(3, 50), (6, 40), (3, 60)]),            # rows of two sequences at once
+    ([0, 100, 1, 101], [(100, 130), (3, 40), (100, 120)]),  # ninety-nine of them
+    ([0, 5, 0, 4, 9], [(5, 60), (2, 30), (4, 44), (5, 70)]),
+    ([4, 9, 2, 2, 6], [(5, 60), (2, 30), (1, 44), (4, 70)])])
+def test_a_sequence_of_decreasing_ends_leaves_its_neighbours_whole(cu, lens, inplace):
+    """Only the sequence whose own ends go back is left out: the others' queries and slots are all
+    written, also of rows that two of them own, each row turned once."""
+    c = Case(lens, 4, 2, 128, 64, seed=104)
+    good = [b for b in range(len(lens)) if cu[b + 1] >= cu[b]]
+    c.d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    g = c.g
+    both = torch.randn(c.T, 8, 128, generator=g).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 16, (1, c.T), generator=g, dtype=torch.int32)
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    dev = both.cuda()
+    qt, kt, vt = dev[:, :4], dev[:, 4:6], dev[:, 6:]
+    q = qt if inplace else torch.full((c.T, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    kp, vp = c.d["k_pool"].clone(), c.d["v_pool"].clone()
+    C.cosa_chunk_write(c.shape, C.RopeParams((64,)), qt, kt, vt, pos.cuda(), freq.cuda(), c.d["cu"], c.d["kv"], c.d["table"], q, kp, vp)
+    torch.cuda.synchronize()
+    assert C.cosa_get_status() == 1
+    x = both.float().numpy().astype(np.float64)
+    wq, wk, wv = x[:, :4] if inplace else np.full((c.T, 4, 128), 7.0), _np(c.k_pool), _np(c.v_pool)
+    # (the turned rows do not depend on the sequence: each good one's are taken from one call)
+    for b in good:
+        wq, wk, wv = K.chunk_write(x[:, :4], x[:, 4:6], x[:, 6:], pos.numpy(), freq.numpy(), (64,), False, False,
+                                   np.array([cu[b], cu[b + 1]]), c.kv[b:b + 1], c.table.numpy()[b:b + 1], wq, wk, wv)
+    tol = lambda w: 2.0**-8 * np.abs(w) + 2.0**-20 * 2 * np.abs(x).max()
+    for got, want in ((q, wq), (kp, wk)):
+        got = _np(got)
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert ((np.abs(got - want) <= tol(want)) | np.isnan(want)).all()
+    assert np.array_equal(_np(vp), wv, equal_nan=True)
