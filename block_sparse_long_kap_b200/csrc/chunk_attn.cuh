@@ -40,28 +40,9 @@
 #include <type_traits>
 
 #include "chunk_common.cuh"
+#include "chunk_list.h"
 
 namespace cosa {
-
-// one tile (pair) of the plan
-struct ChunkTile {
-  int tok0;  // first row of q
-  int ntok;
-  int pos0;  // cache position of that token
-  int b;
-  int jb, nb;  // key blocks, nb >= 1
-  int kv;
-  int prefix;
-};
-static_assert(sizeof(ChunkTile) == 32, "read as two 16-byte words");
-
-// one row of the join list: the CTA whose share starts a tile that it does not finish
-struct ChunkJoin {
-  int ntok;  // 0: none
-  int tok0, hk, pad0;
-  int last;  // the CTA that finishes it
-  int pad1[3];
-};
 
 struct ChunkAttnParams {
   ChunkSeqs seqs;
@@ -85,6 +66,11 @@ struct ChunkAttnParams {
   unsigned long long timeout_ns;
 };
 
+__device__ __forceinline__ ChunkBounds chunk_bounds(const ChunkAttnParams& p) {
+  return ChunkBounds{p.seqs.batch, p.seqs.total_q, p.seqs.max_kv, p.num_kv_heads,
+                     p.tile_tokens * p.nt, p.max_tiles, NUM_SMS};
+}
+
 // Half blocks of 64 keys that nb blocks from one with `keys` keys left on hold.
 __device__ __forceinline__ int half_blocks(int nb, int keys) {
   return min(2 * nb, max((keys + 63) >> 6, 1));
@@ -92,10 +78,6 @@ __device__ __forceinline__ int half_blocks(int nb, int keys) {
 
 // A CTA's walk over its share [w, w_end) of the plan; every role walks by itself.
 struct ChunkWalk {
-  // Units of work that a tile counts for besides its blocks (its Q load, its epilogue): without
-  // them the shares that get many short tiles end last.  Packed documents of 1,500 tokens, for
-  // 0, 1, 2, 3, 4 units: 247, 221, 199, 202, 215 us.
-  static constexpr int SETUP = 2;
   long long w, w_end, per_head;
   int hk, t, n_tiles;
   // the segment
@@ -103,14 +85,20 @@ struct ChunkWalk {
   int jb, nb;       // its blocks
   int part;         // -1: the whole tile; else partial slot 0 (starts inside) / 1
   int lead;         // units of the tile's setup that fall into the share
-  __device__ __forceinline__ bool next(const ChunkTile* tiles, const long long* cum) {
+  // (an entry that does not fit the call is reported, and ends the walk)
+  __device__ __forceinline__ bool next(const ChunkAttnParams& p) {
     if (w >= w_end) return false;
-    const int4 x = __ldcg(reinterpret_cast<const int4*>(tiles + t));
-    const int4 y = __ldcg(reinterpret_cast<const int4*>(tiles + t) + 1);
-    const long long start = hk * per_head + __ldcg(cum + t);
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(p.tiles + t));
+    const int4 y = __ldcg(reinterpret_cast<const int4*>(p.tiles + t) + 1);
+    const long long behind = w - hk * per_head - __ldcg(p.cum + t);
     tile.tok0 = x.x; tile.ntok = x.y; tile.pos0 = x.z; tile.b = x.w;
     tile.jb = y.x; tile.nb = y.y; tile.kv = y.z; tile.prefix = y.w;
-    const int at = (int)(w - start) - SETUP;  // negative: in front of the tile's blocks
+    if (!tile_fits(chunk_bounds(p), tile, behind, hk)) {
+      set_status(COSA_ERR_WORKSPACE);
+      w = w_end;
+      return false;
+    }
+    const int at = (int)behind - CHUNK_SETUP;  // negative: in front of the tile's blocks
     const int off = max(at, 0);
     lead = max(-at, 0);
     const long long left = w_end - w - lead;
@@ -226,7 +214,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkAtt
       d.jb = kmax >= 0 ? kmin >> 7 : 0;
       d.nb = kmax >= 0 ? (kmax >> 7) + 1 - d.jb : 1;
     }
-    const long long before = plan_scan(t < T ? d.nb + ChunkWalk::SETUP : 0, red, total);
+    const long long before = plan_scan(t < T ? d.nb + CHUNK_SETUP : 0, red, total);
     if (t < T) {
       p.tiles[t] = d;
       p.cum[t] = base + before;
@@ -339,7 +327,13 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   pdl_wait();
   ChunkWalk walk;
   walk.n_tiles = __ldcg(prm.n_tiles);
-  walk.per_head = __ldcg(prm.cum + walk.n_tiles);
+  walk.per_head = 0;
+  if (walk.n_tiles >= 0 && walk.n_tiles <= prm.max_tiles) walk.per_head = __ldcg(prm.cum + walk.n_tiles);
+  if (!plan_fits(chunk_bounds(prm), walk.n_tiles, walk.per_head)) {
+    set_status(COSA_ERR_WORKSPACE);
+    walk.n_tiles = 0;
+    walk.per_head = 0;
+  }
   const long long total = walk.per_head * prm.num_kv_heads;
   const long long quota = (total + gridDim.x - 1) / gridDim.x;
   walk.w = min((long long)blockIdx.x * quota, total);
@@ -396,7 +390,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     int it = 0, seg = 0;
     bool ok = true;
     const int qtok_bytes = G * TOK * 128 * (D / 64);
-    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance(), ++seg) {
+    for (; ok && walk.next(prm); walk.advance(), ++seg) {
       const int nt = (NT == 2 && walk.tile.ntok > TOK) ? 2 : 1;
       if (seg > 0 && !wait_warp(b_qempty, (seg - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
@@ -440,7 +434,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     bool ok = true;
     ChunkJoin jn;  // the tile that this share starts and does not finish
     jn.ntok = jn.tok0 = jn.hk = jn.last = 0;
-    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance()) {
+    for (; ok && walk.next(prm); walk.advance()) {
       if (walk.part == 1) {
         jn.tok0 = walk.tile.tok0;
         jn.ntok = walk.tile.ntok;
@@ -516,7 +510,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
     for (; ok; ++seg) {
-      if (!all(walk.next(prm.tiles, prm.cum))) break;
+      if (!all(walk.next(prm))) break;
       const int nb = __shfl_sync(0xffffffffu, walk.nb, 0);
       const int keys0 = __shfl_sync(0xffffffffu, walk.tile.kv - walk.jb * C::KB, 0);
       if (!all(wait(b_qfull, seg & 1))) { ok = false; break; }
@@ -592,7 +586,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
     const int row_tok = row / G, row_g = row - row_tok * G;
     int cnt = 0, nseg = 0;  // half blocks and segments of this tile
     bool ok = true;
-    for (; ok && walk.next(prm.tiles, prm.cum); walk.advance()) {
+    for (; ok && walk.next(prm); walk.advance()) {
       const int ntok = walk.tile.ntok - i * TOK;
       if (ntok <= 0) continue;  // a lone tile: the second group of warps has no rows
       const int token = walk.tile.tok0 + i * TOK + row_tok;
@@ -799,6 +793,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) chunk_combine_kernel(const Ch
   const int4 jn = __ldcg(reinterpret_cast<const int4*>(p.joins + blockIdx.x));
   if (!jn.x) return;  // ntok = 0: this CTA cut no tile
   const int last = __ldcg(&p.joins[blockIdx.x].last);
+  if (!join_fits(chunk_bounds(p), jn.x, jn.y, jn.z, blockIdx.x, last)) {
+    set_status(COSA_ERR_WORKSPACE);
+    return;
+  }
   const int lane = threadIdx.x & 31, G = p.group;
   const int c0 = blockIdx.x, n = last - c0 + 1;
   const int row0 = blockIdx.y * (JOIN_WARPS * JOIN_ROWS) + (threadIdx.x >> 5);

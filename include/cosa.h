@@ -484,7 +484,9 @@ cosa_status_t cosa_chunk_attention_workspace_size(const cosa_chunk_t* shape, siz
  * q_stride; out bf16 [total_q][H_q][D] and lse fp32 [total_q][H_q] (natural log, may be
  * NULL), dense.  From one new token a sequence (decode) to whole prompts.  workspace:
  * at least cosa_chunk_attention_workspace_size bytes, 256-byte aligned, contents on entry
- * do not matter; calls that may overlap on the GPU need one each. */
+ * do not matter; calls that may overlap on the GPU need one each, and nobody may write to it before
+ * the call is done (an entry of its lists that does not fit the call is recorded as
+ * COSA_ERR_WORKSPACE in the status word and not followed). */
 cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_params_t* score,
                                    const void* q, int64_t q_stride, const void* k_pool,
                                    const void* v_pool, const int32_t* page_table,
