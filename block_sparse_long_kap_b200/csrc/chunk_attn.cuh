@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   if (__syncthreads_or(*(volatile int*)&g_status == COSA_ERR_TIMEOUT)) {
     // an earlier launch timed out: nothing is run, and the join (which comes all the same) must
     // not take what the workspace holds for a list
+    // (the plan writes to the workspace: this grid, and the join behind it, end after it)
+    pdl_wait();
     if (tid == 0) prm.joins[blockIdx.x].ntok = 0;
     return;
   }
