@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256, 1)
     mbar_init(b_pv, 1);
     mbar_init(b_done, 1);
     *abort_flag = 0;
+    start_s->nb = *start_off = 0;  // (found below, unless the lengths change meanwhile)
     fence_barrier_init();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -214,47 +215,19 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // ---- this CTA's segments; every role walks by itself
-  struct Walk {
-    long long left;
-    int b, hk, off;
-    ChunkTile tile;
-    int jb, nb, part;
-    bool have;  // tile is that of b
-  } wk;
+  DecodeWalk wk;
   wk.left = w1 - w0;
   wk.hk = hk0;
   wk.b = wk.off = 0;
+  wk.lost = false;
   wk.have = wk.left > 0;
   if (wk.have) {
     wk.tile = *start_s;
     wk.b = wk.tile.b;
     wk.off = *start_off;
   }
-  auto next = [&]() -> bool {
-    if (wk.left <= 0) return false;
-    while (!wk.have) {  // sequences without tokens have no blocks
-      wk.tile = decode_tile(prm, wk.b);
-      wk.have = wk.tile.nb > 0;
-      if (!wk.have && ++wk.b == B) {
-        wk.b = 0;
-        ++wk.hk;
-      }
-    }
-    wk.jb = wk.tile.jb + wk.off;
-    const int rest = wk.tile.nb - wk.off;
-    wk.nb = wk.left < rest ? (int)wk.left : rest;
-    wk.part = wk.off > 0 ? 0 : (wk.nb < wk.tile.nb ? 1 : -1);
-    return true;
-  };
-  auto advance = [&]() {
-    wk.left -= wk.nb;
-    wk.off = 0;
-    wk.have = false;
-    if (++wk.b == B) {
-      wk.b = 0;
-      ++wk.hk;
-    }
-  };
+  auto next = [&]() { return wk.next(B, prm.num_kv_heads, [&](int b) { return decode_tile(prm, b); }); };
+  auto advance = [&]() { wk.advance(B); };
 
   const unsigned long long tmo = prm.timeout_ns;
   const uint32_t abort_at = sb0 + C::OFF_MISC + 4;
@@ -365,6 +338,7 @@ __global__ void __launch_bounds__(256, 1)
       }
     }
     if (lane == 0) {
+      if (wk.lost) set_status(COSA_ERR_INVALID_ARG);
       ChunkJoin* o = prm.joins + blockIdx.x;
       o->ntok = jn.ntok;
       o->tok0 = jn.tok0;

@@ -70,4 +70,50 @@ COSA_HD bool join_fits(const ChunkBounds& n, int ntok, int tok0, int hk, int fir
   return rows_fit(n, tok0, ntok) && hk >= 0 && hk < n.num_kv_heads && last > first && last < n.ctas;
 }
 
+// The walk of one CTA of the single-token form over its share: `left` blocks from block `off` of
+// sequence b's tile on.  It has no list: tile_of(b) works a sequence's tile out from the lengths each time
+// (nb = 0: no tokens).  Lengths that are changed while the kernel runs must not keep it from
+// ending, nor take it outside: where the blocks that the share was cut from are no longer there the
+// walk is over, and `lost` set.
+struct DecodeWalk {
+  long long left;
+  int b, hk, off;
+  ChunkTile tile;
+  int jb, nb, part;
+  bool have;  // tile is that of b
+  bool lost;
+
+  template <typename TileOf>
+  COSA_HD bool next(int batch, int num_kv_heads, const TileOf& tile_of) {
+    if (left <= 0) return false;
+    while (!have && hk < num_kv_heads) {  // sequences without tokens have no blocks
+      tile = tile_of(b);
+      have = tile.nb > 0;
+      if (!have && ++b == batch) {
+        b = 0;
+        ++hk;
+      }
+    }
+    const int rest = tile.nb - off;
+    if (!have || rest <= 0) {
+      lost = true;
+      left = 0;
+      return false;
+    }
+    jb = tile.jb + off;
+    nb = left < rest ? (int)left : rest;
+    part = off > 0 ? 0 : (nb < tile.nb ? 1 : -1);
+    return true;
+  }
+  COSA_HD void advance(int batch) {
+    left -= nb;
+    off = 0;
+    have = false;
+    if (++b == batch) {
+      b = 0;
+      ++hk;
+    }
+  }
+};
+
 }  // namespace cosa

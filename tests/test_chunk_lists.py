@@ -19,6 +19,27 @@ int tile(const ChunkBounds* n, const ChunkTile* t, long long at, int hk) { retur
 int join(const ChunkBounds* n, int ntok, int tok0, int hk, int first, int last) {
   return join_fits(*n, ntok, tok0, hk, first, last);
 }
+// Walks a share; the lengths change from nb0 to nb1 before step `when`.  Returns the segments taken
+// (-1: outside what the lengths at that moment allow), *blocks their sum, *lost whether it broke off.
+int walk(int batch, int heads, const int* nb0, const int* nb1, int when, int b0, int off, int hk, long long left,
+         long long* blocks, int* lost) {
+  DecodeWalk w;
+  w.left = left, w.hk = hk, w.b = b0, w.off = off, w.lost = false, w.have = true;
+  int step = 0;
+  auto tile_of = [&](int b) {
+    ChunkTile t = {};
+    t.b = b, t.jb = 5, t.nb = (step < when ? nb0 : nb1)[b];
+    return t;
+  };
+  w.tile = tile_of(b0);
+  *blocks = 0;
+  for (; w.next(batch, heads, tile_of); w.advance(batch), ++step) {
+    if (w.b < 0 || w.b >= batch || w.hk >= heads || w.nb < 1 || w.jb < 5 || w.jb + w.nb > 5 + w.tile.nb) return -1;
+    *blocks += w.nb;
+  }
+  *lost = w.lost;
+  return step;
+}
 }
 """
 
@@ -92,3 +113,32 @@ def test_what_a_plan_writes_passes(lists):
     wide = Bounds(4096, 1 << 30, 1 << 30, 65535, 256, 1 << 30, 148)
     assert lists.tile(wide, Tile((1 << 30) - 256, 256, 0, 4095, 0, 1 << 23, 1 << 30, 0), (1 << 23) + 1, 65534)
     assert lists.plan(wide, 1 << 30, (1 << 30) * ((1 << 23) + 2))
+
+
+def _walk(L, nb0, nb1, when, b0, off, hk, left, heads=2):
+    n = len(nb0)
+    arr = ctypes.c_int * n
+    blocks, lost = ctypes.c_longlong(0), ctypes.c_int(0)
+    steps = L.walk(n, heads, arr(*nb0), arr(*nb1), when, b0, off, hk, ctypes.c_longlong(left), ctypes.byref(blocks),
+                   ctypes.byref(lost))
+    return steps, blocks.value, bool(lost.value)
+
+
+def test_a_share_is_walked_to_its_end(lists):
+    nb = [3, 0, 1, 7, 0]
+    order = [(h, b, j) for h in range(2) for b in range(5) for j in range(nb[b])]
+    for i, (h, b, j) in enumerate(order):
+        for left in range(1, len(order) - i + 1):
+            steps, blocks, lost = _walk(lists, nb, nb, 99, b, j, h, left)
+            assert blocks == left and not lost and steps == len({x[:2] for x in order[i:i + left]})
+
+
+@pytest.mark.parametrize("after", [[0, 0, 0, 0, 0], [1, 0, 0, 0, 0], [3, 0, 1, 2, 0], [9, 9, 9, 9, 9]])
+def test_a_share_ends_though_its_lengths_change_under_it(lists, after):
+    """Lengths gone to nothing kept the walk from ever ending."""
+    nb = [3, 0, 1, 7, 0]
+    order = [(h, b, j) for h in range(2) for b in range(5) for j in range(nb[b])]
+    for i, (h, b, j) in enumerate(order):
+        for when in range(3):
+            steps, blocks, lost = _walk(lists, nb, after, when, b, j, h, len(order) - i)
+            assert steps >= 0 and blocks <= len(order) - i and (lost or blocks == len(order) - i)
