@@ -5,11 +5,15 @@
 // Both products are taken transposed, so that the 128-row side of the tensor core holds keys
 // and head dims instead of rows that do not exist:
 //   S^T = K Q^T      128 keys x 16 rows
-//   O^T = V^T P^T    128 dims x 16 rows,   V^T read from V as it lies (MN-major A)
+//   O^T = V^T P^T    128 dims x 2 x 16 rows,   V^T read from V as it lies (MN-major A)
 // The tiled form spends eight times the multiplications on this (and, under the power cap that
 // a stream of the whole cache alone comes near, clock with them), and leaves the softmax of a
 // block to the one warp whose rows exist; here a thread owns a key, 128 threads share the
-// block, and P goes to the second product through shared memory (16 x 128 bf16).
+// block, and P goes to the second product through shared memory, as two bf16 halves: rows 0-15
+// bf16(p), rows 16-31 bf16(p - high), together within 2^-16 of p.  The products have time for both in one
+// instruction of 32 columns (201.5 against 201.3 us for the 32 sequences below, 12.2 against 12.0 for the
+// one; as two instructions of 16 each 12.5), O^T comes in two halves that the epilogue adds, and the
+// output's error is that of its own rounding: 1.64e-3 of its norm, where one half left 2.1e-3 to 2.3e-3.
 //
 // The running maximum of a row spans threads: a warp reduces its keys' maxima (one redux a
 // row), the four warps vote whether any row passed its exponent base by 2^8, and only then
@@ -39,7 +43,8 @@ struct DecCfg {
   static constexpr int D = 128, KB = 128, THREADS = 256;
   static constexpr uint32_t BLK_BYTES = KB * D * 2;
   static constexpr uint32_t Q_BYTES = N * D * 2;   // two halves of N x 64
-  static constexpr uint32_t P_BYTES = N * KB * 2;
+  static constexpr int NP = 2 * N;  // rows of P: the high halves of the weights, then the low
+  static constexpr uint32_t P_BYTES = NP * KB * 2;
   static constexpr int KS = 3, VS = 3;
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + KS * BLK_BYTES;
@@ -52,7 +57,7 @@ struct DecCfg {
   static constexpr uint32_t OFF_ROWS = OFF_MISC + 64;        // lo, hi, slope, pos [2][N]
   static constexpr uint32_t OFF_EXCH = OFF_ROWS + 2 * 4 * N * 4;  // [N][4]
   static constexpr uint32_t SMEM = OFF_EXCH + N * 16 + 1024;  // 1024-byte alignment slack
-  static constexpr int TMEM_COLS = 64;  // S at 0 and 16, O at 32
+  static constexpr int TMEM_COLS = 64;  // S at 0 and 16, O at 32 (high) and 48 (low)
   static constexpr float kRescale = 8.0f;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(256, 1)
     // ================= MMA issue (the whole warp walks, one lane issues) ==================
     const uint32_t lead = elect_one();
     constexpr uint32_t ID_QK = idesc_bf16_f32(128, N, 0);
-    constexpr uint32_t ID_PV = idesc_bf16_f32(128, N, 0) | (1u << 15);  // A = V^T, MN-major
+    constexpr uint32_t ID_PV = idesc_bf16_f32(128, C::NP, 0) | (1u << 15);  // A = V^T, MN-major
     const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
     const uint64_t dv = smem_desc_sw128(sV, C::KB * 128, 1024), dp = smem_desc_sw128(sP, 16, 1024);
     int it = 0, seg = 0;
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_bf16_ss_if(k * 16 < keys ? lead : 0u, tmem + 32, dvs + ((k * 16 * 128) >> 4),
-                           dps + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), ID_PV,
+                           dps + (((k >> 2) * (C::NP * 128) + (k & 3) * 32) >> 4), ID_PV,
                            (j > 1 || k > 0) ? 1u : 0u);
           mma_commit_if(lead, b_pv);
           mma_commit_if(lead, b_vempty(s));
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(256, 1)
     const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16);
     float* exch = reinterpret_cast<float*>(sg + C::OFF_EXCH);  // [N][4]
     // where this key's weights go in P: row r at + r * 128, its 16-byte piece swizzled by r
-    const uint32_t p_col = sP + (row >> 6) * (N * 128) + (row & 7) * 2, p_piece = (row & 63) >> 3;
+    const uint32_t p_col = sP + (row >> 6) * (C::NP * 128) + (row & 7) * 2, p_piece = (row & 63) >> 3;
     int cnt = 0, nseg = 0;
     bool ok = true;
     for (; next(); advance()) {
@@ -510,11 +515,14 @@ __global__ void __launch_bounds__(256, 1)
             if (j > 0) {  // O is at rest once the previous block's product is done
               if (wait_warp(b_pv, (cnt - 1) & 1)) {
                 tc_fence_after();
-                uint32_t o[N];
-                tmem_ld16(t_row + 32, o);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t o[N];
+                  tmem_ld16(t_row + 32 + h * N, o);
 #pragma unroll
-                for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
-                tmem_st16(t_row + 32, o);
+                  for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+                  tmem_st16(t_row + 32 + h * N, o);
+                }
                 tmem_st_wait();
               } else {
                 ok = false;
@@ -530,8 +538,10 @@ __global__ void __launch_bounds__(256, 1)
             for (int r = r0; r < r0 + 4; ++r) {
               const float p = ex2_approx(x[r] - (m_ref[r] == -INFINITY ? 0.f : m_ref[r]));
               l[r] += p;
-              st_shared_b16(p_col + buf * C::P_BYTES + r * 128 + ((p_piece ^ (r & 7)) << 4),
-                            __float2bfloat16_rn(p));
+              const __nv_bfloat16 hi = __float2bfloat16_rn(p);
+              const uint32_t at = p_col + buf * C::P_BYTES + r * 128 + ((p_piece ^ (r & 7)) << 4);
+              st_shared_b16(at, hi);
+              st_shared_b16(at + N * 128, __float2bfloat16_rn(p - __bfloat162float(hi)));
             }
           }
           fence_proxy_async_smem();
@@ -557,8 +567,11 @@ __global__ void __launch_bounds__(256, 1)
       named_bar_sync(1, 128);
       if (ok) {
         tc_fence_after();
-        uint32_t o[N];
+        uint32_t o[N], low[N];
         tmem_ld16(t_row + 32, o);
+        tmem_ld16(t_row + 32 + N, low);
+#pragma unroll
+        for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(low[r]));
         const long long slot = (2 * blockIdx.x + (wk.part > 0 ? 1 : 0)) * (long long)prm.part_rows;
         long long at = (long long)wk.tile.tok0 * prm.num_q_heads + wk.hk * G;  // row 0's
         int g = 0;

@@ -482,7 +482,9 @@ cosa_status_t cosa_chunk_attention_workspace_size(const cosa_chunk_t* shape, siz
 /* Exact attention of every sequence's new tokens over its cache (the new tokens' own keys
  * included: queue it after cosa_chunk_write).  q bf16 [total_q][H_q][D] with row stride
  * q_stride; out bf16 [total_q][H_q][D] and lse fp32 [total_q][H_q] (natural log, may be
- * NULL), dense.  From one new token a sequence (decode) to whole prompts.  workspace:
+ * NULL), dense.  From one new token a sequence (decode) to whole prompts.  Scores, sums and lse are
+ * fp32; the weights meet V rounded to bf16 (2^-8 of a weight at most), or within 2^-16 where a sequence
+ * and KV head have at most 16 rows (token, query head) and D = 128.  workspace:
  * at least cosa_chunk_attention_workspace_size bytes, 256-byte aligned, contents on entry
  * do not matter; calls that may overlap on the GPU need one each, and nobody may write to it before
  * the call is done (an entry of its lists that does not fit the call is recorded as

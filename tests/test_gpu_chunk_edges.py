@@ -172,3 +172,20 @@ def test_a_sequence_of_decreasing_ends_leaves_its_neighbours_whole(cu, lens, inp
         assert np.array_equal(np.isnan(got), np.isnan(want))
         assert ((np.abs(got - want) <= tol(want)) | np.isnan(want)).all()
     assert np.array_equal(_np(vp), wv, equal_nan=True)
+
+
+# ---- weights of few rows ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,hq,hk", [([(1, 2049)], 32, 8), ([(1, 700), (2, 1300), (0, 9)], 28, 4), ([(4, 515)], 16, 4)])
+@pytest.mark.parametrize("opt", ["plain", "cap", "bias+prefix"])
+def test_few_rows_keep_their_weights_whole(lens, hq, hk, opt):
+    """Up to 16 rows at D = 128 the weights meet V as two bf16 halves, 2^-16 of them at most left over:
+    beside the scores only the result's own rounding is seen."""
+    c = Case(lens, hq, hk, 128, 64, seed=106)
+    score, kw = c.score(opt)
+    out, lse = c.attend(score)
+    o, l, spread = c.oracle(kw)
+    n, ds = int(c.cu[-1]), c.ds(kw)
+    # fp32 sums over the keys: n 2^-24 of the spread at most, in the products and in the divisor
+    tol = (2.0**-16 + 2 * ds + 2 * int(c.kv.max()) * 2.0**-24) * spread + 2.0**-8 * np.abs(o)
+    assert (np.abs(_np(out) - o)[:n] <= tol[:n]).all()
+    assert C.cosa_get_status() == 0
