@@ -189,3 +189,120 @@ def test_few_rows_keep_their_weights_whole(lens, hq, hk, opt):
     tol = (2.0**-16 + 2 * ds + 2 * int(c.kv.max()) * 2.0**-24) * spread + 2.0**-8 * np.abs(o)
     assert (np.abs(_np(out) - o)[:n] <= tol[:n]).all()
     assert C.cosa_get_status() == 0
+
+
+# ---- large prompts ------------------------------------------------------------------------------------------
+def _exact_rows(q, k_pool, v_pool, table, kv, scale, pos0):
+    """Causal attention of consecutive tokens of one sequence in 64 bits on the GPU, [tokens][H_q][D]:
+    out, lse, sum of w |v|, sum of w^2 v^2."""
+    n, hq, hk, P = q.shape[0], q.shape[1], k_pool.shape[1], k_pool.shape[2]
+    key = torch.arange(kv, device="cuda")
+    pages = table.long()[key // P]
+    res = []
+    for h in range(hq):
+        K_, V_ = (x[pages, h // (hq // hk), key % P].double() for x in (k_pool, v_pool))
+        x = q[:, h].double() @ K_.T * scale
+        x.masked_fill_(key[None] > pos0 + torch.arange(n, device="cuda")[:, None], -float("inf"))
+        w = torch.softmax(x, -1)
+        res.append((w @ V_, torch.logsumexp(x, -1), w @ V_.abs(), (w * w) @ (V_ * V_)))
+    return [torch.stack(r, 1) for r in zip(*res)]
+
+
+LARGE = [
+    ([(1024, 1024)], 8, 2, 128, 64),               # the whole prompt
+    ([(1100, 3001)], 8, 2, 128, 64),               # a piece of one: pairs of tiles cut between CTAs
+    ([(1531, 7000)], 4, 4, 64, 16),
+    ([(700, 4100), (1, 2000), (1300, 1300)], 7, 1, 128, 128),
+]
+
+
+def _check_large(out, lse, ref, ds, kv):
+    o, l, spread, w2v2 = ref
+    err = (out.double() - o).abs()
+    # for any signs of the roundings
+    assert (err <= (2.0**-8 + 2 * ds) * spread + 2.0**-8 * o.abs()).all()
+    assert ((lse.double() - l).abs() <= ds + kv * 2.0**-24 + 2.0**-22 * l.abs()).all()
+    # The weights' roundings are independent from key to key, each of mean square (2^-8 w)^2 / 3 at most
+    # (uniform over half a step of up to 2^-8), so an element's error has a mean square of
+    # (2^-8)^2 / 3 (sum w^2 v^2 + o^2); summed over the elements of a row, three times that, and the
+    # scores' share for any signs.  A half block of values lost or doubled is ten times as much.
+    rms = (2.0**-8) * (w2v2 + o * o).sum(-1).sqrt()
+    assert (err.norm(dim=-1) <= rms + 2 * ds * spread.norm(dim=-1)).all()
+
+
+@pytest.mark.parametrize("lens,hq,hk,D,P", LARGE)
+def test_every_element_of_a_large_prompt(lens, hq, hk, D, P):
+    """Over a thousand keys random values average to a twentieth of their size: the bounds are those of an
+    element's own size and spread, not of V's."""
+    c = Case(lens, hq, hk, D, P, seed=107)
+    out, lse = c.attend()
+    for b, (n, kv) in enumerate(lens):
+        rows = slice(int(c.cu[b]), int(c.cu[b]) + n)
+        ref = _exact_rows(c.d["q"][rows], c.d["k_pool"], c.d["v_pool"], c.d["table"][b], kv, c.scale, kv - n)
+        _check_large(out[rows], lse[rows], ref, c.ds({}), kv)
+    assert C.cosa_get_status() == 0
+
+
+# ---- the prompt's path and the chunks' on one cache ------------------------------------------------------------
+@pytest.mark.parametrize("D,P", [(128, 64), (64, 64), (128, 128)])
+def test_a_sparse_prefill_decoded_by_chunks(D, P):
+    """cosa_prefill_write and the ordered-skipping attention take the prompt (head-major q and lse), the
+    chunk calls what comes after it (token-major), on the same pools and page table; the cache is cut and
+    decoded on."""
+    N, hq, hk, B, budget = 1024, 8, 2, 2, 400
+    g = torch.Generator().manual_seed(108)
+    pps, need = N // P + 2, -(-budget // P) + 1
+    phys = B * (pps + need) + 3
+    perm = torch.randperm(phys, generator=g).to(torch.int32)
+    table, dst = perm[:B * pps].view(B, pps).cuda(), perm[B * pps:B * (pps + need)].view(B, need).cuda()
+    kp, vp = (torch.full((phys, hk, P, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tok = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+    q_tok, k_tok, v_tok = tok(B, N, hq, D), tok(B, N, hk, D), tok(B, N, hk, D)
+    sh = C.Shape(B, hq, hk, N, D, P, 128, pages_per_seq=pps, num_phys_pages=phys)
+    kap = C.KapParams(budget=1.0, q_sub=32, k_sub=16, sink_pages=1)
+    q = torch.empty(B, hq, N, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(C.cosa_kap_workspace_size(sh, kap), dtype=torch.uint8, device="cuda")
+    C.cosa_prefill_write(sh, kap, q_tok, k_tok, v_tok, table, q, kp, vp, workspace=ws)
+    order = torch.empty(B, hq, N // 128, C.cosa_kap_kcap(sh, kap), dtype=torch.int32, device="cuda")
+    count = torch.empty(B, hq, N // 128, dtype=torch.int32, device="cuda")
+    C.cosa_kap_rank(sh, kap, order, count, ws)
+    out, lse = torch.empty_like(q), torch.empty(B, hq, N, device="cuda")
+    C.cosa_osk_attention(sh, C.OskParams(eps=0.0), q, kp, vp, table, order, count, out, lse=lse)
+    ds = D * 2.0**-24 * D**-0.5 * float(q_tok.float().norm(dim=-1).max() * k_tok.float().norm(dim=-1).max())
+    # all pages, none skipped: the chunk attention of the whole prompt over the same cache agrees
+    s = C.ChunkShape(B, hq, hk, D, P, B * N, N, N, pps, phys)
+    cu, kv = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, N, 2 * N], [N, N]))
+    wsc = torch.empty(C.cosa_chunk_attention_workspace_size(s), dtype=torch.uint8, device="cuda")
+    o2, l2 = torch.empty(B * N, hq, D, dtype=torch.bfloat16, device="cuda"), torch.empty(B * N, hq, device="cuda")
+    C.cosa_chunk_attention(s, q_tok.view(B * N, hq, D), kp, vp, table, cu, kv, o2, wsc, lse=l2)
+    mass = torch.zeros(B, hk, pps * P, device="cuda")
+    C.cosa_attention_mass(s, q_tok.view(B * N, hq, D), kp, table, cu, kv, l2, mass, last_q=16)
+    for b in range(B):
+        ref = _exact_rows(q_tok[b], kp, vp, table[b], N, D**-0.5, 0)
+        _check_large(out[b].transpose(0, 1), lse[b].T, ref, ds, N)
+        _check_large(o2[b * N:b * N + N], l2[b * N:b * N + N], ref, ds, N)
+
+    def step(lens, kv, table):
+        T, width = sum(lens), table.shape[1]
+        s = C.ChunkShape(B, hq, hk, D, P, T, max(lens), int(max(kv)), width, phys)
+        x = tok(T, hq + 2 * hk, D)
+        cu, kvd = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, lens[0], T], list(kv)))
+        qt, o, l = x[:, :hq], torch.empty(T, hq, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, hq, device="cuda")
+        w = torch.empty(C.cosa_chunk_attention_workspace_size(s), dtype=torch.uint8, device="cuda")
+        C.cosa_chunk_write(s, None, qt, x[:, hq:hq + hk], x[:, hq + hk:], None, None, cu, kvd, table, qt, kp, vp)
+        C.cosa_chunk_attention(s, qt, kp, vp, table, cu, kvd, o, w, lse=l)
+        wo, wl, spread = K.chunk_attention(_np(qt), _np(kp), _np(vp), _np(table), _np(cu), np.array(kv), D**-0.5)
+        assert (np.abs(_np(o) - wo) <= (2.0**-8 + 4 * ds) * spread + 2.0**-8 * np.abs(wo)).all()
+        assert (np.abs(_np(l) - wl) <= 2 * ds + N * 2.0**-23 + 2.0**-22 * np.abs(wl)).all()
+        return s, kvd
+
+    step([1, 1], [N + 1, N + 1], table)
+    s, kvd = step([40, 1], [N + 41, N + 2], table)
+    kept = torch.empty(B, hk, budget, dtype=torch.int32, device="cuda")
+    n = torch.empty(B, dtype=torch.int32, device="cuda")
+    C.cosa_cache_evict(s, C.EvictParams(budget, sink=4, recent=64), kp, vp, table, kvd, mass, dst[:, :-(-budget // P)].contiguous(),
+                       kept, n)
+    assert n.tolist() == [budget, budget]
+    step([1, 1], [budget + 1, budget + 1], dst)  # the page after the kept keys' is the next one to fill
+    step([3, 20], [budget + 4, budget + 21], dst)
+    assert C.cosa_get_status() == 0
