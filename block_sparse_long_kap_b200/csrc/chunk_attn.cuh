@@ -377,11 +377,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   const int pshift = 31 - __clz(P);        // P is a power of two
   const int ppb = C::KB >> pshift;         // pages a block, at most 8: one a lane
   // coordinate of page `lane` of block j (-1: outside the pool, read as zeros)
-  auto page_coord = [&](int b, int hk, int j, int np) -> int {
+  auto page_coord = [&](const ChunkTile& tile, int hk, int j, int np) -> int {
     if (lane >= np) return 0;
-    const int ph = __ldg(prm.page_table + (long long)b * prm.pages_per_seq + j * ppb + lane);
+    const int ph = __ldg(prm.page_table + (long long)tile.b * prm.pages_per_seq + j * ppb + lane);
     if (ph < 0 || ph >= prm.num_phys_pages) {
-      set_status(COSA_ERR_INVALID_ARG);
+      if ((j * ppb + lane + 1) << pshift > window_start(prm.mask, tile.pos0)) set_status(COSA_ERR_INVALID_ARG);
       return -1;
     }
     return ph * prm.num_kv_heads + hk;
@@ -409,12 +409,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       }
       constexpr int DIR = REV ? -1 : 1;
       int jx = walk.jb + (REV ? walk.nb - 1 : 0);
-      int cz = page_coord(walk.tile.b, walk.hk, jx, blk_pages(walk.tile.kv, jx));
+      int cz = page_coord(walk.tile, walk.hk, jx, blk_pages(walk.tile.kv, jx));
       for (int j = 0; j < walk.nb; ++j, ++it, jx += DIR) {
         const int s = it % C::KS, np = blk_pages(walk.tile.kv, jx);
         int cz_next = 0;
         if (j + 1 < walk.nb)
-          cz_next = page_coord(walk.tile.b, walk.hk, jx + DIR, blk_pages(walk.tile.kv, jx + DIR));
+          cz_next = page_coord(walk.tile, walk.hk, jx + DIR, blk_pages(walk.tile.kv, jx + DIR));
         if (it >= C::KS && !wait_warp(b_kempty(s), ((it / C::KS) - 1) & 1)) { ok = false; break; }
         if (lane == 0) mbar_arrive_expect_tx(b_kfull(s), (uint32_t)(np * P * D * 2));
         __syncwarp();
@@ -449,13 +449,13 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       }
       constexpr int DIR = REV ? -1 : 1;
       int jx = walk.jb + (REV ? walk.nb - 1 : 0);
-      int cz = page_coord(walk.tile.b, walk.hk, jx, blk_pages(walk.tile.kv, jx));
+      int cz = page_coord(walk.tile, walk.hk, jx, blk_pages(walk.tile.kv, jx));
       for (int j = 0; j < walk.nb; ++j, ++it, jx += DIR) {
         const int s = it % C::VS, np = blk_pages(walk.tile.kv, jx);
         const int keys = walk.tile.kv - jx * C::KB;
         int cz_next = 0;
         if (j + 1 < walk.nb)
-          cz_next = page_coord(walk.tile.b, walk.hk, jx + DIR, blk_pages(walk.tile.kv, jx + DIR));
+          cz_next = page_coord(walk.tile, walk.hk, jx + DIR, blk_pages(walk.tile.kv, jx + DIR));
         if (it >= C::VS && !wait_warp(b_vempty(s), ((it / C::VS) - 1) & 1)) { ok = false; break; }
         // the MMA reads the keys of whole 16-key steps: those behind the end are zeroed
         const bool tail = keys < C::KB && (keys & 15) != 0;

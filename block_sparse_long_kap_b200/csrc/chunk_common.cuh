@@ -107,6 +107,12 @@ __device__ __forceinline__ void token_range(const ChunkMask& m, int token, int p
   hi = min(max(pos, max(prefix, 0) - 1), kv - 1);
 }
 
+// The first key that the window leaves to the token at position pos and to those after it.  What the
+// page table says of pages before it does not matter: a server gives them up.
+__device__ __forceinline__ int window_start(const ChunkMask& m, int pos) {
+  return m.window > 0 ? pos - m.window + 1 : 0;
+}
+
 // Pairs of floats in one 64-bit register: the FMA pipe takes both in one instruction.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {

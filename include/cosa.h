@@ -410,7 +410,8 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * (Where cu_q goes back, two of them may own a row: cosa_chunk_write writes it to both caches,
  * cosa_chunk_attention leaves the result of either in it.)  A page-table entry
  * outside the pool is recorded the same way; its keys read as zeros and nothing is
- * written there.  Keys are addressed by cache position: after an eviction, positions
+ * written there.  (Pages that lie before the window of all the tokens at hand may have been given
+ * up: their entries are not looked at.)  Keys are addressed by cache position: after an eviction, positions
  * (and the window and distances below) count the kept keys, while the rotation of
  * cosa_chunk_write takes its own position values. */
 typedef struct {

@@ -306,3 +306,76 @@ def test_a_sparse_prefill_decoded_by_chunks(D, P):
     step([1, 1], [budget + 1, budget + 1], dst)  # the page after the kept keys' is the next one to fill
     step([3, 20], [budget + 4, budget + 21], dst)
     assert C.cosa_get_status() == 0
+
+
+# ---- pages that a window has left behind ------------------------------------------------------------------------
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("q,D", FORMS)
+def test_pages_before_the_window_may_be_given_up(q, D, P):
+    """Their entries name nothing, wherever in a block of keys they end: no error, and every key that a token
+    sees is there.  A page with one such key is still missed."""
+    window = 70
+    c = Case([(q, 700), (q, 333)], 4, 2, D, P, seed=109)
+    kw, score = dict(window=window), C.ScoreParams(window=window)
+    keep = [(kv - q - window + 1) // P for q, kv in c.lens]  # the first page that the first token sees
+    for b, n in enumerate(keep):
+        c.d["table"][b, :max(n, 0)] = -1
+    out, lse = c.attend(score)
+    _check_rows(c, out, lse, kw, c.ds({}))
+    old = torch.rand(2, 2, c.pps * P, generator=c.g)
+    for last in (0, 1):
+        mass = old.cuda()
+        C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, score=score, last_q=last)
+        want = K.attention_mass(_np(c.q), _np(c.k_pool), c.table.numpy(), c.cu, c.kv, _np(lse), _np(old), c.scale, last_q=last, **kw)
+        rel = c.ds({}) + 2.0**-22 * (np.abs(_np(lse)[:2 * q]).max() + 2) + q * 2 * 2.0**-24
+        for b, (_, kv) in enumerate(c.lens):
+            assert (np.abs(_np(mass) - want)[b, :, :kv] <= rel * want[b, :, :kv] + 1e-30).all()
+    assert C.cosa_get_status() == 0
+    c.d["table"][1, keep[1]] = -1
+    c.attend(score)
+    assert C.cosa_get_status() == 1
+    C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, score=score)
+    assert C.cosa_get_status() == 1
+
+
+# ---- more sequences than threads --------------------------------------------------------------------------------
+@pytest.mark.parametrize("D,qs", [(128, (1, 0, 2)), (64, (1, 3, 0)), (128, (1, 40, 0))])
+def test_batches_past_a_block_of_threads(D, qs):
+    """1,300 sequences: past the 256, 384 and 1,024 threads that list them in one go."""
+    g = torch.Generator().manual_seed(110)
+    B, P = 1300, 16
+    kvs = torch.randint(41, 60, (B,), generator=g).tolist()
+    c = Case([(qs[b % 3], kvs[b]) for b in range(B)], 4, 2, D, P, seed=111)
+    out, lse = c.attend()
+    _check_rows(c, out, lse, {}, c.ds({}))
+    _check_mass_of_full(c, lse)
+    both = torch.randn(c.T, 8, D, generator=g).to(torch.bfloat16).cuda()
+    kp, vp = c.d["k_pool"].clone(), c.d["v_pool"].clone()
+    q = torch.full((c.T, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    C.cosa_chunk_write(c.shape, None, both[:, :4], both[:, 4:6], both[:, 6:], None, None, c.d["cu"], c.d["kv"], c.d["table"], q, kp, vp)
+    assert C.cosa_get_status() == 0
+    n = int(c.cu[-1])
+    seq = np.repeat(np.arange(B), np.diff(c.cu))
+    pos = c.kv[seq] - c.cu[seq + 1] + np.arange(n)
+    page, slot = c.table.long()[seq, pos // P], torch.from_numpy(pos % P)
+    assert torch.equal(q[:n], both[:n, :4]) and (q[n:] == 7).all()
+    wk, wv = c.d["k_pool"].clone(), c.d["v_pool"].clone()
+    wk[page, :, slot], wv[page, :, slot] = both[:n, 4:6], both[:n, 6:]
+    assert torch.equal(torch.nan_to_num(kp.float(), 99.0), torch.nan_to_num(wk.float(), 99.0))
+    assert torch.equal(torch.nan_to_num(vp.float(), 99.0), torch.nan_to_num(wv.float(), 99.0))
+
+
+def _check_mass_of_full(c, lse):
+    """A key's mass, and with it each sequence's: a token gives its group's heads one each."""
+    mass = torch.full((len(c.lens), c.hk, c.pps * c.P), 5.0, device="cuda")
+    C.cosa_attention_mass(c.shape, c.d["q"], c.d["k_pool"], c.d["table"], c.d["cu"], c.d["kv"], lse, mass, decay=0.0)
+    assert C.cosa_get_status() == 0
+    ds = c.ds({}) + 2.0**-22 * 12 + 60 * 2.0**-24
+    got = _np(mass)
+    for b, (n, kv) in enumerate(c.lens):
+        if n == 0:
+            assert (got[b] == 5).all()
+            continue
+        assert (np.abs(got[b, :, :kv].sum(-1) - n * c.hq // c.hk) <= ds * (n * c.hq // c.hk)).all()
+        assert (got[b, :, kv:] == 5).all()
+
