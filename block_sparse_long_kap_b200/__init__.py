@@ -843,7 +843,7 @@ def cosa_cache_evict(shape: ChunkShape, evict: EvictParams, k_pool, v_pool, page
     bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     s, e, dev = shape.c(), evict.c(), _current_device()
     _, _, _, dpool, dtab, _, dkv, dmass = shape.dims()
-    n, hk, pages = s.batch, s.num_kv_heads, -(-e.budget // s.page_size)
+    n, hk, pages = s.batch, s.num_kv_heads, -(-e.budget // max(s.page_size, 1))
     st = lib().cosa_cache_evict(
         ctypes.byref(s), ctypes.byref(e), _arg(k_pool, "k_pool", bf, dpool, dev),
         _arg(v_pool, "v_pool", bf, dpool, dev), _arg(page_table, "page_table", i32, dtab, dev),

@@ -164,3 +164,16 @@ def test_caps_past_what_fp32_can_double_are_refused(cap):
     ref, sc = ctypes.byref(s), ctypes.byref(p)
     assert L.cosa_chunk_attention(ref, sc, 16, 1024, 16, 16, 16, 16, 16, 16, None, 256, ws, None) == 1
     assert L.cosa_attention_mass(ref, sc, 16, 1024, 16, 16, 16, 16, 16, 0, 1.0, 16, None) == 1
+
+
+@pytest.mark.parametrize("page_size", [0, -16])
+def test_binding_of_the_eviction_names_what_is_wrong_with_the_shape(monkeypatch, page_size):
+    """(a page size of zero divided the budget)"""
+    monkeypatch.setattr(C, "_current_device", lambda: -1)  # where host tensors say they are
+    s = C.ChunkShape(**{**GOOD, "page_size": page_size})
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    stream = type("Stream", (), {"cuda_stream": 0})
+    with pytest.raises((C.CosaError, ValueError), match="cosa_cache_evict: |shape"):
+        pool = torch.zeros(8, 2, max(page_size, 0), 128, dtype=torch.bfloat16)
+        C.cosa_cache_evict(s, C.EvictParams(10), pool, pool, i32(2, 4), i32(2), torch.zeros(2, 2, 0), i32(2, 10), i32(2, 2, 10), i32(2),
+                           stream=stream)
