@@ -360,6 +360,18 @@ def _timed(fn, reps, stream, warm=1):
     return e0.elapsed_time(e1) / reps
 
 
+# Legs with a table each.  They go to stderr as a JSON line of their own: with them the result line is 20 KB,
+# which a reader of the last few KB of a run's output does not get whole.
+TABLE_LEGS = ("eps_sweep", "group_shared", "early_break", "preskip", "decode", "fused_write", "budget_sweep")
+
+
+def emit(line, out=None, err=None):
+    tables = {k: line[k] for k in TABLE_LEGS if k in line}
+    if tables:
+        print(json.dumps({"legs": tables}), file=err or sys.stderr, flush=True)
+    print(json.dumps({k: v for k, v in line.items() if k not in tables}), file=out or sys.stdout, flush=True)
+
+
 # Per-budget sweep (the speedup over the own dense kernel at each budget, and the ordered
 # against the page-order visit): workload -> (budgets, eps values, visit orders)
 SWEEP = (
@@ -971,7 +983,7 @@ def main():
     line["cpu_baseline"] = {"value": fl / secs / 1e12, "unit": "TFLOP/s", "cores": threads,
                             "host_cores": _cpu_cores(), "kind": "oracle", "sample": desc,
                             "extrapolated_full_layer_s": dense_flop / (fl / secs)}
-    print(json.dumps(line), flush=True)
+    emit(line)
     return 0
 
 

@@ -153,3 +153,19 @@ def test_kap_pool_bytes_closed_form():
     # two fp32 terms: 8 * 128 * (32 * 4096 + 8 * 8192) bytes
     b = bench.kap_pool_bytes(1, 32, 8, 131072, 128, 32, 16)
     assert b == 2 * 131072 * 128 * 40 + 8 * 128 * (32 * 4096 + 8 * 8192)
+
+
+def test_result_line_is_short_and_whole_without_the_legs_tables():
+    import io
+    import json
+    contract = {"metric": "m", "value": 1.5, "unit": "TFLOP/s", "n_gpus": 1, "steps": 20, "warmup": 5, "ms_per_step": 2.0,
+                "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+                "config": {"model": "x"}, "gpu_launches": 80, "clocks": {"sm_mhz": 1965.0}, "e2e": {"value": 1.0},
+                "roofline": {"frac": 0.5}, "dense": {"ms": 1.0}}
+    tables = {k: [{"x": 1.0 / 3.0}] * 100 for k in bench.TABLE_LEGS}
+    out, err = io.StringIO(), io.StringIO()
+    bench.emit({**contract, **tables}, out, err)
+    lines = out.getvalue().splitlines()
+    assert len(lines) == 1 and json.loads(lines[0]) == contract and len(lines[0]) < 3000
+    assert json.loads(err.getvalue()) == {"legs": tables}
+
