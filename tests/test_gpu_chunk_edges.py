@@ -379,3 +379,174 @@ def _check_mass_of_full(c, lse):
         assert (np.abs(got[b, :, :kv].sum(-1) - n * c.hq // c.hk) <= ds * (n * c.hq // c.hk)).all()
         assert (got[b, :, kv:] == 5).all()
 
+
+
+# ---- calls that nothing above makes ------------------------------------------------------------------------------
+@pytest.mark.parametrize("scale", [1e-3, 0.7])
+@pytest.mark.parametrize("q,D", FORMS)
+def test_a_scale_of_the_callers(q, D, scale):
+    c = Case([(q, 400), (q, 130)], 4, 2, D, 64, seed=112)
+    c.shape.softmax_scale = scale
+    c.scale = np.float32(scale).item()
+    kw, score = dict(softcap=50.0), C.ScoreParams(softcap=50.0)
+    for kw, score in (({}, None), (kw, score)):
+        out, lse = c.attend(score)
+        _check_rows(c, out, lse, kw, c.ds(kw))
+        _check_mass(c, score, kw, lse, c.ds(kw))
+
+
+@pytest.mark.parametrize("q", [1, 3])
+def test_no_lse_asked_of_the_few_row_form(q):
+    c = Case([(q, 3000), (q, 100)], 8, 2, 128, 64, seed=113)
+    out, _ = c.attend()
+    ws = torch.empty(C.cosa_chunk_attention_workspace_size(c.shape), dtype=torch.uint8, device="cuda")
+    out2 = torch.full_like(out, 7.0)
+    C.cosa_chunk_attention(c.shape, c.d["q"], c.d["k_pool"], c.d["v_pool"], c.d["table"], c.d["cu"], c.d["kv"], out2, ws)
+    assert torch.equal(out, out2)
+
+
+class _Server:
+    """One decode step and the cut behind it: write, attention, mass, eviction, on its own buffers."""
+
+    def __init__(self, seed, D=128, P=32, B=3, pps=40, budget=300):
+        g = torch.Generator().manual_seed(seed)
+        hq, hk, need = 8, 2, -(-budget // P)
+        phys = B * (pps + need)
+        perm = torch.randperm(phys, generator=g).to(torch.int32)
+        r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+        self.kp, self.vp = r(phys, hk, P, D), r(phys, hk, P, D)
+        self.table, self.dst = perm[:B * pps].view(B, pps).cuda(), perm[B * pps:].view(B, need).cuda()
+        self.x = r(B, hq + 2 * hk, D)
+        self.kv = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        self.pos = torch.zeros(1, B, dtype=torch.int32, device="cuda")
+        self.freq = (10000.0 ** (-torch.arange(D // 2) / (D // 2))).float().cuda()
+        self.shape = C.ChunkShape(B, hq, hk, D, P, B, 1, pps * P, pps, phys)
+        self.q = torch.empty(B, hq, D, dtype=torch.bfloat16, device="cuda")
+        self.out, self.lse = torch.empty_like(self.q), torch.empty(B, hq, device="cuda")
+        self.ws = torch.empty(C.cosa_chunk_attention_workspace_size(self.shape), dtype=torch.uint8, device="cuda")
+        self.mass = torch.rand(B, hk, pps * P, generator=g).cuda()
+        self.kept = torch.empty(B, hk, budget, dtype=torch.int32, device="cuda")
+        self.n = torch.empty(B, dtype=torch.int32, device="cuda")
+        self.small = torch.empty(B, hk, need * P, device="cuda")
+        self.evict, self.hq, self.hk = C.EvictParams(budget, 4, 50), hq, hk
+        self.state = {k: v.clone() for k, v in vars(self).items() if torch.is_tensor(v)}
+
+    def set(self, kv):
+        for k, v in self.state.items():
+            getattr(self, k).copy_(v)
+        self.kv.copy_(torch.tensor(kv, dtype=torch.int32))
+        self.pos.copy_(self.kv[None] - 1)
+
+    def run(self, stream=None):
+        h, k = self.hq, self.hk
+        C.cosa_chunk_write(self.shape, C.RopeParams((self.freq.numel(),)), self.x[:, :h], self.x[:, h:h + k], self.x[:, h + k:],
+                           self.pos, self.freq, self.cu, self.kv, self.table, self.q, self.kp, self.vp, stream=stream)
+        C.cosa_chunk_attention(self.shape, self.q, self.kp, self.vp, self.table, self.cu, self.kv, self.out, self.ws, lse=self.lse,
+                               stream=stream)
+        C.cosa_attention_mass(self.shape, self.q, self.kp, self.table, self.cu, self.kv, self.lse, self.mass, stream=stream)
+        C.cosa_cache_evict(self.shape, self.evict, self.kp, self.vp, self.table, self.kv, self.mass, self.dst, self.kept, self.n,
+                           mass_out=self.small, stream=stream)
+
+    def result(self):
+        torch.cuda.synchronize()
+        res = [x.clone() for x in (self.kp, self.vp, self.q, self.out, self.lse, self.mass, self.kept, self.n)]
+        for b, n in enumerate(self.n.tolist()):
+            res.append(self.small[b, :, :n].clone())
+        return res
+
+
+LENGTHS = [[1, 1280, 299], [301, 300, 700], [1024, 33, 1279]]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_whole_step_captured_and_replayed_with_other_lengths(D):
+    s = _Server(114, D)
+    want = []
+    for kv in LENGTHS:
+        s.set(kv)
+        s.run()
+        want.append(s.result())
+    s.set(LENGTHS[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.run()
+    for kv, w in zip(LENGTHS, want):
+        s.set(kv)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(s.result(), w))
+    assert C.cosa_get_status() == 0
+
+
+def test_two_whole_steps_at_once_on_two_streams():
+    a, b = _Server(115), _Server(116, 64, 16, pps=80)
+    want = []
+    for s in (a, b):
+        s.set(LENGTHS[2])
+        s.run()
+        want.append(s.result())
+        s.set(LENGTHS[2])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s, st in zip((a, b), streams):
+        s.run(stream=st)
+    for s, w in zip((a, b), want):
+        assert all(torch.equal(x, y) for x, y in zip(s.result(), w))
+    assert C.cosa_get_status() == 0
+
+
+def test_pools_and_rows_past_what_32_bits_count():
+    """Pages and query rows whose elements lie past 2^31, and tokens at the end of a long row list."""
+    P, hk, hq, D, n = 64, 2, 4, 128, 5
+    phys = 2**31 // (hk * P * D) + 40
+    kp, vp = (torch.empty(phys, hk, P, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    T, width = 270000, 8000  # 2.16e9 elements of a fused projection
+    fused = torch.empty(T, width, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(117)
+    kv, pps = 1000, 16
+    table = torch.arange(phys - 20, phys - 20 + pps, dtype=torch.int32)[None]
+    small = [torch.randn(pps, hk, P, D, generator=g).to(torch.bfloat16) for _ in range(2)]
+    for pool, x in zip((kp, vp), small):
+        pool[phys - 20:phys - 20 + pps] = x.cuda()
+    tok = torch.randn(n, (hq + 2 * hk) * D, generator=g).to(torch.bfloat16)
+    fused[T - n:, :tok.shape[1]] = tok.cuda()
+    rows = fused[:, :tok.shape[1]].view(T, hq + 2 * hk, D)
+    sh = C.ChunkShape(1, hq, hk, D, P, T, n, kv, pps, phys)
+    cu, kvd = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([T - n, T], [kv]))
+    td = table.cuda()
+    qr = rows[:, :hq]
+    C.cosa_chunk_write(sh, None, qr, rows[:, hq:hq + hk], rows[:, hq + hk:], None, None, cu, kvd, td, qr, kp, vp)
+    out = torch.zeros(T, hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(T, hq, device="cuda")
+    ws = torch.empty(C.cosa_chunk_attention_workspace_size(sh), dtype=torch.uint8, device="cuda")
+    mass = torch.zeros(1, hk, pps * P, device="cuda")
+    xs = tok.view(n, hq + 2 * hk, D).float().numpy().astype(np.float64)
+    q, (sk, sv) = xs[:, :hq], (_np(x) for x in small)
+    near = np.arange(pps)[None]
+    _, sk, sv = K.chunk_write(q, xs[:, hq:hq + hk], xs[:, hq + hk:], None, None, (), False, False, np.array([0, n]),
+                              np.array([kv]), near, q, sk, sv)
+    o, l, spread = K.chunk_attention(q, sk, sv, near, np.array([0, n]), np.array([kv]), D**-0.5)
+    ds = D * 2.0**-24 * D**-0.5 * np.linalg.norm(q, axis=-1).max() * np.linalg.norm(sk, axis=-1).max()
+    C.cosa_chunk_attention(sh, qr, kp, vp, td, cu, kvd, out, ws, lse=lse)
+    assert (np.abs(_np(out[T - n:]) - o) <= (2.0**-8 + 2 * ds) * spread + 2.0**-8 * np.abs(o)).all()
+    assert (np.abs(_np(lse[T - n:]) - l) <= ds + kv * 2.0**-24 + 2.0**-22 * np.abs(l)).all()
+    sh.max_q = kv  # a looser bound: the tiled form
+    ws = torch.empty(C.cosa_chunk_attention_workspace_size(sh), dtype=torch.uint8, device="cuda")
+    out.zero_()
+    C.cosa_chunk_attention(sh, qr, kp, vp, td, cu, kvd, out, ws, lse=lse)
+    assert (np.abs(_np(out[T - n:]) - o) <= (2.0**-8 + 2 * ds) * spread + 2.0**-8 * np.abs(o)).all()
+    assert not out[:T - n].any()
+    C.cosa_attention_mass(sh, qr, kp, td, cu, kvd, lse, mass)
+    want = K.attention_mass(q, sk, near, np.array([0, n]), np.array([kv]), _np(lse[T - n:]), np.zeros((1, hk, pps * P)), D**-0.5)
+    rel = ds + 2.0**-22 * (np.abs(l).max() + 2) + n * 2 * 2.0**-24
+    assert (np.abs(_np(mass) - want) <= rel * want + 1e-30).all()
+    dst = torch.arange(phys - 4, phys, dtype=torch.int32, device="cuda")[None]
+    kept, left = torch.empty(1, hk, 200, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    C.cosa_cache_evict(sh, C.EvictParams(200, 4, 20), kp, vp, td, kvd, mass, dst, kept, left)
+    assert C.cosa_get_status() == 0 and int(left) == 200
+    for h in range(hk):
+        src = _np(kept)[0, h]
+        assert (np.diff(src) > 0).all()
+        for pool, x in ((kp, sk), (vp, sv)):
+            got = _np(pool[phys - 4:])[:, h].reshape(-1, D)[:200]
+            assert np.array_equal(got, x[src // P, h, src % P])
