@@ -251,10 +251,12 @@ __global__ void __launch_bounds__(384, 1)
         const int s = x % C::KS, np = min(ppb, (r.seq.kv - kb * C::KB + P - 1) >> pshift);
         int cz = 0;
         if (lane < np) {
-          const int ph = __ldg(prm.page_table + (long long)r.b * prm.pages_per_seq + kb * ppb + lane);
-          cz = (ph < 0 || ph >= prm.num_phys_pages) ? -1 : ph * prm.num_kv_heads + r.hk;
-          if (cz < 0 && (kb * ppb + lane + 1) << pshift > window_start(prm.mask, r.pos0))
-            set_status(COSA_ERR_INVALID_ARG);
+          cz = -1;
+          if ((kb * ppb + lane + 1) << pshift > window_start(prm.mask, r.pos0)) {
+            const int ph = __ldg(prm.page_table + (long long)r.b * prm.pages_per_seq + kb * ppb + lane);
+            if (ph >= 0 && ph < prm.num_phys_pages) cz = ph * prm.num_kv_heads + r.hk;
+            else set_status(COSA_ERR_INVALID_ARG);
+          }
         }
         if (x >= C::KS && !wait_warp(b_kempty(s), ((x / C::KS) - 1) & 1)) { ok = false; break; }
         if (lane == 0) mbar_arrive_expect_tx(b_kfull(s), (uint32_t)(np * P * D * 2));

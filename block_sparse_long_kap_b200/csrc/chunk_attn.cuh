@@ -376,12 +376,13 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   };
   const int pshift = 31 - __clz(P);        // P is a power of two
   const int ppb = C::KB >> pshift;         // pages a block, at most 8: one a lane
-  // coordinate of page `lane` of block j (-1: outside the pool, read as zeros)
+  // coordinate of page `lane` of block j (-1: outside the pool or given up, read as zeros)
   auto page_coord = [&](const ChunkTile& tile, int hk, int j, int np) -> int {
     if (lane >= np) return 0;
+    if ((j * ppb + lane + 1) << pshift <= window_start(prm.mask, tile.pos0)) return -1;
     const int ph = __ldg(prm.page_table + (long long)tile.b * prm.pages_per_seq + j * ppb + lane);
     if (ph < 0 || ph >= prm.num_phys_pages) {
-      if ((j * ppb + lane + 1) << pshift > window_start(prm.mask, tile.pos0)) set_status(COSA_ERR_INVALID_ARG);
+      set_status(COSA_ERR_INVALID_ARG);
       return -1;
     }
     return ph * prm.num_kv_heads + hk;

@@ -107,8 +107,10 @@ __device__ __forceinline__ void token_range(const ChunkMask& m, int token, int p
   hi = min(max(pos, max(prefix, 0) - 1), kv - 1);
 }
 
-// The first key that the window leaves to the token at position pos and to those after it.  What the
-// page table says of pages before it does not matter: a server gives them up.
+// The first key that the window leaves to the token at position pos and to those after it.  Pages
+// before it read as zeros whatever the page table says: a server gives them up, and their entries
+// may name nothing, or a page that holds something else by now (NaN too, which a weight of zero
+// would not keep out of the second product).
 __device__ __forceinline__ int window_start(const ChunkMask& m, int pos) {
   return m.window > 0 ? pos - m.window + 1 : 0;
 }

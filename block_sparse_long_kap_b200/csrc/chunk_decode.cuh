@@ -249,9 +249,10 @@ __global__ void __launch_bounds__(256, 1)
   auto blk_pages = [&](int kv, int j) { return min(ppb, (kv - j * C::KB + P - 1) >> pshift); };
   auto page_coord = [&](int j, int np) -> int {
     if (lane >= np) return 0;
+    if ((j * ppb + lane + 1) << pshift <= window_start(prm.mask, wk.tile.pos0)) return -1;
     const int ph = __ldg(prm.page_table + (long long)wk.b * prm.pages_per_seq + j * ppb + lane);
     if (ph < 0 || ph >= prm.num_phys_pages) {
-      if ((j * ppb + lane + 1) << pshift > window_start(prm.mask, wk.tile.pos0)) set_status(COSA_ERR_INVALID_ARG);
+      set_status(COSA_ERR_INVALID_ARG);
       return -1;
     }
     return ph * prm.num_kv_heads + wk.hk;

@@ -411,7 +411,7 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * cosa_chunk_attention leaves the result of either in it.)  A page-table entry
  * outside the pool is recorded the same way; its keys read as zeros and nothing is
  * written there.  (Pages that lie before the window of all the tokens at hand may have been given
- * up: their entries are not looked at.)  Keys are addressed by cache position: after an eviction, positions
+ * up: neither their entries nor what they name is looked at.)  Keys are addressed by cache position: after an eviction, positions
  * (and the window and distances below) count the kept keys, while the rotation of
  * cosa_chunk_write takes its own position values. */
 typedef struct {
@@ -459,9 +459,9 @@ typedef struct {
 } cosa_score_params_t;
 /* A token at position t sees key k iff k < kv_len, k >= max(first_key, t - window + 1),
  * and k <= t or k < prefix_len.  A token that sees no key gets a zero output row and lse
- * -inf.  Keys and values at and past kv_len may hold anything (NaN included); V of the keys
- * below kv_len must be finite, since a value that one row of a tile does not see is
- * multiplied by a zero weight. */
+ * -inf.  Keys and values at and past kv_len, and in pages before the window, may hold anything (NaN
+ * included); V of the other keys below kv_len must be finite, since a value that one row of a tile
+ * does not see is multiplied by a zero weight. */
 
 /* Rotate and append: writes q[token] = rotate(q_tok[token]) and, at each token's cache
  * position, K = rotate(k_tok) and V = v_tok.  positions int32 [axes][total_q] and
@@ -484,8 +484,8 @@ cosa_status_t cosa_chunk_attention_workspace_size(const cosa_chunk_t* shape, siz
  * included: queue it after cosa_chunk_write).  q bf16 [total_q][H_q][D] with row stride
  * q_stride; out bf16 [total_q][H_q][D] and lse fp32 [total_q][H_q] (natural log, may be
  * NULL), dense.  From one new token a sequence (decode) to whole prompts.  Scores, sums and lse are
- * fp32; the weights meet V rounded to bf16 (2^-8 of a weight at most), or within 2^-16 where a sequence
- * and KV head have at most 16 rows (token, query head) and D = 128.  workspace:
+ * fp32; the weights meet V rounded to bf16 (2^-8 of a weight at most), or within 2^-16 where D = 128 and
+ * max_q * H_q / H_kv <= 16.  workspace:
  * at least cosa_chunk_attention_workspace_size bytes, 256-byte aligned, contents on entry
  * do not matter; calls that may overlap on the GPU need one each, and nobody may write to it before
  * the call is done (an entry of its lists that does not fit the call is recorded as

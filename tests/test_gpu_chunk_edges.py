@@ -309,17 +309,21 @@ def test_a_sparse_prefill_decoded_by_chunks(D, P):
 
 
 # ---- pages that a window has left behind ------------------------------------------------------------------------
+@pytest.mark.parametrize("entry", ["none", "another's"])
 @pytest.mark.parametrize("P", [16, 64])
 @pytest.mark.parametrize("q,D", FORMS)
-def test_pages_before_the_window_may_be_given_up(q, D, P):
-    """Their entries name nothing, wherever in a block of keys they end: no error, and every key that a token
-    sees is there.  A page with one such key is still missed."""
+def test_pages_before_the_window_may_be_given_up(q, D, P, entry):
+    """Their entries name nothing, or a page that holds something else by now (NaN), wherever in a block of
+    keys they end: no error, and every key that a token sees is there.  A page with one such key is still
+    missed."""
     window = 70
     c = Case([(q, 700), (q, 333)], 4, 2, D, P, seed=109)
     kw, score = dict(window=window), C.ScoreParams(window=window)
     keep = [(kv - q - window + 1) // P for q, kv in c.lens]  # the first page that the first token sees
+    free = sorted(set(range(c.phys)) - set(c.table.flatten().tolist()))[0]
+    assert torch.isnan(c.v_pool[free].float()).all()
     for b, n in enumerate(keep):
-        c.d["table"][b, :max(n, 0)] = -1
+        c.d["table"][b, :max(n, 0)] = -1 if entry == "none" else free
     out, lse = c.attend(score)
     _check_rows(c, out, lse, kw, c.ds({}))
     old = torch.rand(2, 2, c.pps * P, generator=c.g)
