@@ -21,7 +21,8 @@
 // takes 43 us, 0.78 of a copy's rate, the rest is the start of the stream and the last pair's
 // way through.  For many rows by the exponentials (16 a cycle and SM): the last 64 tokens of 32
 // heads on 64K keys are 134 M of them, 30 us, and take 62 us (special-function unit 50 % busy,
-// tensor core 25 %); a quarter of them as a polynomial on the FMA pipe gave nothing.
+// tensor core 25 %); a quarter of them as a polynomial on the FMA pipe gave nothing.  All 2,048 tokens of a
+// chunk on 8K keys (470 M of them, 103 us at the unit's rate) take 257 us, the unit 56 % busy.
 // A softmax warp whose wait ran out keeps meeting the others at their named barrier, so that
 // none waits there for good.
 #pragma once

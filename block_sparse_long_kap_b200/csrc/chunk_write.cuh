@@ -8,9 +8,10 @@
 // pair serves all heads, so the table of a CTA's tokens is made once in shared memory.
 // The work is the copy: every element is read and written once, 16 bytes a lane.
 //
-// Measured: 32K tokens of 80 heads (1.33 GB) 223 us, 0.91 of a copy's rate; 8,191 tokens of 36
-// heads (151 MB) 33 us, where launch, table and tail are a quarter; a decode step of 64
-// sequences 3.3 us, its table and one trip to memory.  Deeper unrolling (2 to 4 units a thread
+// Measured: 32K tokens of 80 heads (1.33 GB) 224 us, 0.91 of a copy's rate; 8,191 tokens of 36
+// heads (151 MB) 33 us called, 30.5 replayed, 23 of them its bytes': each CTA's first loads come behind its page
+// lookup, its table and a barrier, and the issue slots are 56 % busy, a division a unit among what
+// fills them; a decode step of 64 sequences 3.3 us, its table and one trip to memory.  Deeper unrolling (2 to 4 units a thread
 // in flight) took 249 to 364 us for the first.
 #pragma once
 

@@ -518,8 +518,9 @@ ChunkLayout chunk_layout(const cosa_chunk_t* s) {
   const int G = s->num_q_heads / s->num_kv_heads, tok = 128 / G;
   // one tile at a time while a sequence's rows fit in it: the pair's second softmax group would
   // be idle, a V slot fewer is left and the partial rows take more room.  Measured, one tile
-  // against a pair, D = 64: 7 rows of 32 sequences 189 against 193 us, one sequence of 2K keys 14.7
-  // against 15.2 us; at 20 to 128 rows both are within the runs' spread
+  // against a pair, D = 64: 7 rows of 32 sequences 189 against 193 us (their bytes alone take 98: both
+  // spend 128 rows of products on 7), one sequence of 2K keys 14.7 against 15.2 us; at 20 to 128 rows
+  // both are within the runs' spread
   L.nt = s->max_q <= tok ? 1 : 2;
   L.part_rows = L.nt == 2 ? 256 : s->max_q * G;
   const size_t span = (size_t)tok * L.nt;
@@ -1392,7 +1393,7 @@ cosa_status_t cosa_chunk_attention(const cosa_chunk_t* shape, const cosa_score_p
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Up to 16 rows a sequence: both products transposed.  Measured on 32 ragged sequences of up to
   // 32K keys, transposed against tiled: 7 rows 199 against 208 us (205 against 231 in long runs),
-  // one sequence of 2K keys 11.9 against 17.8 us; 28 rows (32 columns) 208 against 185 us.
+  // one sequence of 2K keys 12.1 against 17.8 us; 28 rows (32 columns) 208 against 185 us.
   if (shape->head_dim == 128 && shape->max_q * p.group <= DecCfg::N)
     return launch_decode_chunk(shape, p, cap != CAP_NONE, q, q_stride, k_pool, v_pool, st);
   if (shape->head_dim == 128)
@@ -1486,7 +1487,8 @@ cosa_status_t cosa_cache_evict(const cosa_chunk_t* shape, const cosa_evict_param
   p.recent = evict->recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the largest segment's keys held in shared memory, where they fit beside the histograms
-  // (a 32K cache: 18 against 24 us with the masses read again in every pass)
+  // (both kernels back to back on a 32K cache, before other steps: 18 against 24 us with the masses read
+  // again in every pass; 20.4 us now, from cold caches)
   const int seg = (shape->max_kv + EVICT_CL - 1) / EVICT_CL;
   dim3 clusters(EVICT_CL, shape->num_kv_heads, shape->batch);
   if (seg <= EVICT_SEG_MAX) {

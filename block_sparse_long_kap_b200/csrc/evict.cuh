@@ -11,8 +11,9 @@
 // bytes a cycle).  Equal masses at the border go to the lowest positions: the CTAs' counts
 // of larger and of equal keys give each one its place, so the kept list comes out ascending
 // and is the same on every run.
-// Measured: 32K keys of 8 heads cut to 4K 20 us on the device, six ragged sequences of up to 16K keys
-// 26 us; the bytes are 5 and 8 us of it.  The rest is latency in a chain: three digits of
+// Measured, both kernels replayed back to back: 32K keys of 8 heads cut to 4K 20.4 us, six ragged
+// sequences of up to 16K keys 25.7 us; the bytes are 5 and 8 us of it.  (Apart and from cold caches the select
+// takes 16 us in both, the gather 12 and 16.)  The rest is latency in a chain: three digits of
 // counting, cluster barrier and scan, the placing, the gather's two dependent
 // loads.
 // evict_gather_kernel: a copy, 16 bytes a lane, source pages never written.

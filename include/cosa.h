@@ -70,7 +70,8 @@ typedef enum {
   COSA_ERR_UNSUPPORTED = 2, /* valid but outside the supported shape set        */
   COSA_ERR_CUDA = 3,        /* a CUDA runtime/driver call or a launch failed     */
   COSA_ERR_TIMEOUT = 4,     /* a kernel's bounded wait ran out (status word)     */
-  COSA_ERR_WORKSPACE = 5    /* workspace missing or smaller than required        */
+  COSA_ERR_WORKSPACE = 5    /* workspace missing or smaller than required; in the
+                               status word: written to while a call used it      */
 } cosa_status_t;
 
 /* Problem shape shared by all entry points. */
@@ -408,7 +409,8 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * q_len > max_q, kv_len > max_kv or q_len > kv_len is recorded as COSA_ERR_INVALID_ARG in
  * the status word and left out (its outputs keep what they held); the others are served in full.
  * (Where cu_q goes back, two of them may own a row: cosa_chunk_write writes it to both caches,
- * cosa_chunk_attention leaves the result of either in it.)  A page-table entry
+ * cosa_chunk_attention leaves the result of either in it, and runs nothing if they add up to more
+ * tiles than total_q rows and batch sequences can give.)  A page-table entry
  * outside the pool is recorded the same way; its keys read as zeros and nothing is
  * written there.  (Pages that lie before the window of all the tokens at hand may have been given
  * up: neither their entries nor what they name is looked at.)  Keys are addressed by cache position: after an eviction, positions
