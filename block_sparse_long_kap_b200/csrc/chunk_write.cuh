@@ -77,7 +77,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // counted one is not its own.  (Such a cu_q is an error and recorded as one; the sequences that are
 // sound have to come out whole, not fast.)  q is written with a token's first sequence only: in
 // place, a second turn would count.
-__device__ __forceinline__ void chunk_write_review(const ChunkWriteParams& p, int D) {
+__device__ __forceinline__ void chunk_write_look_over(const ChunkWriteParams& p, int D) {
   const int tid = threadIdx.x, hq = p.num_q_heads, hk = p.num_kv_heads;
   bool back = false;
   for (int b = tid; b < p.seqs.batch; b += CHUNK_WRITE_THREADS) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(CHUNK_WRITE_THREADS, 6)
   const int n = min(p.tokens_per_cta, p.seqs.total_q - tok0);
   const int half = p.half;
   if (n <= 0) {  // the CTA past the last token
-    if (blockIdx.y == 0) chunk_write_review(p, D);
+    if (blockIdx.y == 0) chunk_write_look_over(p, D);
     return;
   }
   // the sequence of token t: the number of sequences that end at or before it

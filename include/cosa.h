@@ -413,9 +413,9 @@ cosa_status_t cosa_debug_osk_wait_fault(int32_t withhold_k_group, uint64_t wait_
  * tiles than total_q rows and batch sequences can give.)  A page-table entry
  * outside the pool is recorded the same way; its keys read as zeros and nothing is
  * written there.  (Pages that lie before the window of all the tokens at hand may have been given
- * up: neither their entries nor what they name is looked at.)  Keys are addressed by cache position: after an eviction, positions
- * (and the window and distances below) count the kept keys, while the rotation of
- * cosa_chunk_write takes its own position values. */
+ * up: neither their entries nor what they name is looked at.)  Keys are addressed by cache
+ * position: after an eviction, positions (and the window and distances below) count the kept keys,
+ * while the rotation of cosa_chunk_write takes its own position values. */
 typedef struct {
   int32_t batch;          /* B, at most 4096                                       */
   int32_t num_q_heads;    /* H_q                                                   */

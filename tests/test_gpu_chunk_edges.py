@@ -554,3 +554,20 @@ def test_pools_and_rows_past_what_32_bits_count():
         for pool, x in ((kp, sk), (vp, sv)):
             got = _np(pool[phys - 4:])[:, h].reshape(-1, D)[:200]
             assert np.array_equal(got, x[src // P, h, src % P])
+
+
+@pytest.mark.parametrize("opt", ["plain", "cap", "prefix", "window"])
+@pytest.mark.parametrize("q,D", FORMS)
+def test_slopes_of_either_sign(q, D, opt):
+    """A falling, a rising and no slope at all side by side: far keys ahead of near ones in some heads."""
+    c = Case([(q, 1900), (q, 130)], 8, 2, D, 64, seed=118)
+    score, kw = c.score(opt)
+    kw["slopes"] = np.array([0.5, -0.5, 0.0, -0.01, 2.0, -2.0, 0.001, -30.0], np.float32)
+    score.slopes = torch.from_numpy(kw["slopes"]).cuda()
+    out, lse = c.attend(score)
+    # the bias is rounded as a product with log2 e and as a sum: 2^-22 of it, where it weighs at all (within
+    # 60 of the row's largest, which is at a distance of 1900 at most)
+    ds = c.ds(kw) + 1900 * 30.0 * 2.0**-22
+    _check_rows(c, out, lse, kw, ds)
+    _check_mass(c, score, kw, lse, ds)
+    assert C.cosa_get_status() == 0
