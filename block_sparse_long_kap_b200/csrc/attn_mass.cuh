@@ -238,11 +238,18 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) okl = wait(bar_addr, parity) ? 1 : 0;
     return __shfl_sync(0xffffffffu, okl, 0) != 0;
   };
+  // A loader that is ahead waits for whole pairs: a K slot comes free once all the chunk's tiles have
+  // passed it (a tile takes a pair one to two microseconds; half a million of them were past the
+  // limit), held tiles once the CTA's pairs of their sequence are through.  Its limit grows with that.
+  auto wait_long = [&](uint32_t bar_addr, uint32_t parity, long long steps) -> bool {
+    return mbar_try_wait(bar_addr, parity) || wait_on(bar_addr, parity, abort_at, tmo + 20000ull * steps);
+  };
   auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
 
   if (warp == 0) {
     // ================= K ==============================================================
     const int pshift = 31 - __clz(P), ppb = C::KB >> pshift;
+    const int most_tiles = (prm.seqs.max_q + TOK - 1) / TOK;
     int x = 0;  // blocks loaded
     bool ok = true;
     for (; ok && r.p < last; next()) {
@@ -259,7 +266,11 @@ __global__ void __launch_bounds__(384, 1)
             else set_status(COSA_ERR_INVALID_ARG);
           }
         }
-        if (x >= C::KS && !wait_warp(b_kempty(s), ((x / C::KS) - 1) & 1)) { ok = false; break; }
+        if (x >= C::KS) {
+          int free = 1;
+          if (lane == 0) free = wait_long(b_kempty(s), ((x / C::KS) - 1) & 1, prm.held ? 0 : most_tiles) ? 1 : 0;
+          if (!__shfl_sync(0xffffffffu, free, 0)) { ok = false; break; }
+        }
         if (lane == 0) mbar_arrive_expect_tx(b_kfull(s), (uint32_t)(np * P * D * 2));
         __syncwarp();
         if (lane < np)
@@ -287,7 +298,10 @@ __global__ void __launch_bounds__(384, 1)
         const int ta = prm.held ? 0 : r.t0, tb = prm.held ? C::QS : r.t1;
         for (int t = ta; t < tb; ++t) {
           const int s = x % C::QS;
-          if (x >= C::QS && !wait(b_qempty(s), ((x / C::QS) - 1) & 1)) { ok = false; break; }
+          if (x >= C::QS && !wait_long(b_qempty(s), ((x / C::QS) - 1) & 1, prm.held ? share : 0)) {
+            ok = false;
+            break;
+          }
           mbar_arrive_expect_tx(b_qfull(s), bytes);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)

@@ -46,3 +46,13 @@ def test_a_dependent_kernel_waits_before_its_first_way_out(name):
     assert wait >= 0 and (first is None or wait < first.start())
     # and again where the early way out is not taken
     assert first is None or body.count("pdl_wait()") >= (2 if name == "chunk_attn_kernel" else 1)
+
+
+def test_the_mass_loaders_allow_for_the_work_they_are_ahead_of():
+    """A slot of theirs comes free after whole pairs of key blocks, not after one hand-off: a limit that
+    does not grow with the chunk's tiles would end a long one as a timeout."""
+    body = _body("attn_mass_kernel")
+    waits = re.findall(r"(\w+)\(b_[kq]empty\(s\), [^;{]*?, (.*?)\) *[?)]", body)
+    assert [w[0] for w in waits] == ["wait_long", "wait_long"]
+    assert "most_tiles" in waits[0][1] and "share" in waits[1][1]
+    assert re.search(r"tmo \+ \d+ull \* steps", body)
