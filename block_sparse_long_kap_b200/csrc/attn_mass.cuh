@@ -78,7 +78,7 @@ struct MassCfg {
   static_assert(OFF_CUM + (CHUNK_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory budget");
 };
 
-template <int D, CapForm CAP, bool BIAS>  // CAP: none, far, each
+template <int D, CapForm CAP, bool BIAS>  // CAP: none, or each where not all are near
 __global__ void __launch_bounds__(384, 1)
     attn_mass_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k, const MassParams prm) {
@@ -450,15 +450,16 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) continue;
         tc_fence_after();
         const float fkey = (float)(key - r.pos0);
-        auto add = [&](auto mask_tag, const uint32_t* v, int c0) {  // 16 rows
+        auto add_as = [&](auto mask_tag, auto form_tag, const uint32_t* v, int c0) {  // 16 rows
           constexpr bool MASK = decltype(mask_tag)::value;
+          constexpr CapForm FORM = decltype(form_tag)::value;
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(m->c + c0 + e);
-            f32x2 x0 = score2_log2<CAP>(
+            f32x2 x0 = score2_log2<FORM>(
                 prm.score, pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
                 pack2(c4.x, c4.y));
-            f32x2 x1 = score2_log2<CAP>(
+            f32x2 x1 = score2_log2<FORM>(
                 prm.score, pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
                 pack2(c4.z, c4.w));
             if (BIAS) {
@@ -483,6 +484,19 @@ __global__ void __launch_bounds__(384, 1)
             sum[0] = add2(sum[0], pack2(y[0], y[1]));
             sum[1] = add2(sum[1], pack2(y[2], y[3]));
           }
+        };
+        auto add = [&](auto mask_tag, const uint32_t* v, int c0) {
+          if (CAP) {
+            float far = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              far = fmax3f(far, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+            if (__all_sync(0xffffffffu, far <= prm.score.lim)) {
+              add_as(mask_tag, std::integral_constant<CapForm, CAP_NEAR>{}, v, c0);
+              return;
+            }
+          }
+          add_as(mask_tag, std::integral_constant<CapForm, CAP>{}, v, c0);
         };
         auto sweep = [&](auto mask_tag) {
           const uint32_t t_s = t_row + sbuf * 128;

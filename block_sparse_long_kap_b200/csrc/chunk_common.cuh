@@ -151,15 +151,17 @@ __device__ __forceinline__ f32x2 both(float a) { return pack2(a, a); }
 //                  here, but for a small score under a large cap all of it (9e-3 at a cap of
 //                  10^5).  (The hardware tanh, relative error 2^-11, would move a logit near a cap
 //                  of 50 by 0.02.)
-// The first form leaves the special-function unit two results an element: the tiled attention's warps
-// take it (CAP_NEAR) where all their scores are in its range, the usual case.  For the others, and
-// for the mass:
-//   CAP_FAR   the second form for all scores, up to a cap of 64: its error is at most 2^-17 there, two
-//             roundings of a score of 64
-//   CAP_EACH  larger caps: chosen for each score.  (For all caps it took 276 against 242 us on packed
-//             documents, 149 against 121 us for the mass of 64 tokens on 64K keys, both with scores
-//             beyond their cap of 2.  In the single-token form, bound by its bytes, it costs nothing
-//             and is taken for all: 200 us for 32 ragged sequences either way.)
+// The first form leaves the special-function unit two results an element: the tiled attention and the
+// mass take it (CAP_NEAR) where all of a warp's scores are in its range, the usual case.  For the
+// others:
+//   CAP_FAR   the second form for all scores: the tiled attention under caps up to 64, where its error is at
+//             most 2^-17, two roundings of a score of 64, and far below that of its weights
+//   CAP_EACH  chosen for each score: the tiled attention under larger caps, the mass (a sum of weights
+//             as they are), the single-token form for all scores.  (In the tiled attention on packed
+//             documents, scores beyond their cap of 2: 276 against 242 us.  In the mass of 64 tokens on
+//             64K keys, where CAP_FAR for all takes 121 us whatever the cap: 90 us under a cap of 30,
+//             149 under one of 2.  In the single-token form, bound by its bytes, 200 us for 32 ragged
+//             sequences either way.)
 enum CapForm { CAP_NONE, CAP_NEAR, CAP_FAR, CAP_EACH };
 constexpr float kCapFarMax = 64.f;
 struct ScoreShape {

@@ -691,7 +691,8 @@ template <int D>
 cosa_status_t launch_mass_d(const cosa_chunk_t* s, const MassParams& prm, CapForm cap, const void* q,
                             int64_t q_stride, const void* k_pool, cudaStream_t st) {
   auto go = [&](auto form, auto bias) {
-    return launch_mass_t<D, decltype(form)::value, decltype(bias)::value>(s, prm, q, q_stride, k_pool, st);
+    constexpr CapForm F = decltype(form)::value == CAP_NONE ? CAP_NONE : CAP_EACH;
+    return launch_mass_t<D, F, decltype(bias)::value>(s, prm, q, q_stride, k_pool, st);
   };
   return with_form(cap, prm.slopes, go);
 }

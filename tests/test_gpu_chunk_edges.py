@@ -571,3 +571,15 @@ def test_slopes_of_either_sign(q, D, opt):
     _check_rows(c, out, lse, kw, ds)
     _check_mass(c, score, kw, lse, ds)
     assert C.cosa_get_status() == 0
+
+
+@pytest.mark.parametrize("cap", [5.0, 50.0])
+@pytest.mark.parametrize("q,D", [(1, 64), (20, 64), (300, 64), (2, 128), (200, 128)])
+def test_mass_under_a_cap_is_as_exact_as_without(q, D, cap):
+    """Small scores: the cap's own error, 2^-20 of a score, is next to nothing beside the fp32 product's."""
+    c = Case([(q, 700), (min(q, 90), 90)], 4, 2, D, 64, seed=119, spread=0.01)
+    kw, score = dict(softcap=cap), C.ScoreParams(softcap=cap)
+    ds = c.ds({}) + 2.0**-20 * c.ds({}) / (D * 2.0**-24)
+    out, lse = c.attend(score)
+    _check_mass(c, score, kw, lse, ds)
+
