@@ -85,51 +85,58 @@ __device__ __forceinline__ void chunk_write_look_over(const ChunkWriteParams& p,
     back |= __ldg(p.seqs.cu_q + b + 1) < __ldg(p.seqs.cu_q + b);
   }
   if (!__syncthreads_or(back)) return;
-  for (int t = 0; t < p.seqs.total_q; ++t) {
+  // a warp a token
+  const int lane = tid & 31;
+  for (int t = tid >> 5; t < p.seqs.total_q; t += CHUNK_WRITE_THREADS / 32) {
     int counted = 0;
-    for (int b = 0; b < p.seqs.batch; ++b) counted += __ldg(p.seqs.cu_q + b + 1) <= t;
-    auto owns = [&](int b, ChunkSeq& s) {
-      s = chunk_seq(p.seqs, b);
+    for (int b = lane; b < p.seqs.batch; b += 32) counted += __ldg(p.seqs.cu_q + b + 1) <= t;
+    counted = warp_sum_int(counted);
+    auto owns = [&](int b) {
+      const ChunkSeq s = chunk_seq(p.seqs, b);
       return s.ok && t >= s.q0 && t < s.q0 + s.q_len;
     };
-    ChunkSeq s;
-    bool with_q = counted >= p.seqs.batch || !owns(counted, s);
-    for (int b = 0; b < p.seqs.batch; ++b) {
-      if (b == counted || !owns(b, s)) continue;
-      const int pos = s.kv - s.q_len + (t - s.q0);
-      const int phys = __ldg(p.page_table + (long long)b * p.pages_per_seq + pos / p.page_size);
-      const bool page = phys >= 0 && phys < p.num_phys_pages;
-      if (!page) set_status(COSA_ERR_INVALID_ARG);
-      const long long row = (long long)phys * hk * p.page_size + pos % p.page_size;
-      // a thread's item: two elements of a head, a pair that turns together or two that stay
-      for (int x = tid; x < (hq + 2 * hk) * (D / 2); x += CHUNK_WRITE_THREADS) {
-        const int h = x / (D / 2), j = x % (D / 2), g = h < hq ? h : (h - hq) % hk;
-        const bool is_v = h >= hq + hk;
-        if (h < hq ? !with_q : !page) continue;
-        const __nv_bfloat16* src = h < hq ? p.q_tok + t * p.q_tok_stride
-                                          : (is_v ? p.v_tok + t * p.v_tok_stride : p.k_tok + t * p.k_tok_stride);
-        __nv_bfloat16* dst = h < hq ? p.q + t * p.q_stride + g * D
-                                    : (is_v ? p.v_pool : p.k_pool) + (row + (long long)g * p.page_size) * D;
-        src += g * D;
-        const bool halves = j < p.half && !p.adjacent;
-        const int e0 = halves ? j : 2 * j, e1 = halves ? j + p.half : 2 * j + 1;
-        const __nv_bfloat16 x0 = src[e0], x1 = src[e1];
-        if (is_v || j >= p.half) {
-          dst[e0] = x0;
-          dst[e1] = x1;
-          continue;
+    bool with_q = counted >= p.seqs.batch || !owns(counted);
+    for (int b0 = 0; b0 < p.seqs.batch; b0 += 32) {
+      const int mine = b0 + lane;
+      uint32_t owners = __ballot_sync(0xffffffffu, mine < p.seqs.batch && mine != counted && owns(mine));
+      for (; owners; owners &= owners - 1) {
+        const int b = b0 + __ffs(owners) - 1;
+        const ChunkSeq s = chunk_seq(p.seqs, b);
+        const int pos = s.kv - s.q_len + (t - s.q0);
+        const int phys = __ldg(p.page_table + (long long)b * p.pages_per_seq + pos / p.page_size);
+        const bool page = phys >= 0 && phys < p.num_phys_pages;
+        if (!page) set_status(COSA_ERR_INVALID_ARG);
+        const long long row = (long long)phys * hk * p.page_size + pos % p.page_size;
+        // a lane's item: two elements of a head, a pair that turns together or two that stay
+        for (int x = lane; x < (hq + 2 * hk) * (D / 2); x += 32) {
+          const int h = x / (D / 2), j = x % (D / 2), g = h < hq ? h : (h - hq) % hk;
+          const bool is_v = h >= hq + hk;
+          if (h < hq ? !with_q : !page) continue;
+          const __nv_bfloat16* src = h < hq ? p.q_tok + t * p.q_tok_stride
+                                            : (is_v ? p.v_tok + t * p.v_tok_stride : p.k_tok + t * p.k_tok_stride);
+          __nv_bfloat16* dst = h < hq ? p.q + t * p.q_stride + g * D
+                                      : (is_v ? p.v_pool : p.k_pool) + (row + (long long)g * p.page_size) * D;
+          src += g * D;
+          const bool halves = j < p.half && !p.adjacent;
+          const int e0 = halves ? j : 2 * j, e1 = halves ? j + p.half : 2 * j + 1;
+          const __nv_bfloat16 x0 = src[e0], x1 = src[e1];
+          if (is_v || j >= p.half) {
+            dst[e0] = x0;
+            dst[e1] = x1;
+            continue;
+          }
+          // (not shared with the kernel below: in a common function it cost that a spilled register,
+          // and 1 % of the time of 32K tokens)
+          const int at = __ldg(p.positions + (long long)rope_axis(p, j) * p.seqs.total_q + t);
+          const double w = (double)at * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
+          float sn, co;
+          sincospif(2.f * (float)(w - rint(w)), &sn, &co);
+          const float a = __bfloat162float(x0), c = __bfloat162float(x1);
+          dst[e0] = __float2bfloat16_rn(a * co - c * sn);
+          dst[e1] = __float2bfloat16_rn(c * co + a * sn);
         }
-        // (not shared with the kernel below: in a common function it cost that a spilled register, and
-        // 1 % of the time of 32K tokens)
-        const int at = __ldg(p.positions + (long long)rope_axis(p, j) * p.seqs.total_q + t);
-        const double w = (double)at * (double)__ldg(p.inv_freq + j) * 0.15915494309189533577;
-        float sn, co;
-        sincospif(2.f * (float)(w - rint(w)), &sn, &co);
-        const float a = __bfloat162float(x0), c = __bfloat162float(x1);
-        dst[e0] = __float2bfloat16_rn(a * co - c * sn);
-        dst[e1] = __float2bfloat16_rn(c * co + a * sn);
+        with_q = false;
       }
-      with_q = false;
     }
   }
 }

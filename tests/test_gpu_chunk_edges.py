@@ -583,3 +583,35 @@ def test_mass_under_a_cap_is_as_exact_as_without(q, D, cap):
     out, lse = c.attend(score)
     _check_mass(c, score, kw, lse, ds)
 
+
+def test_a_decreasing_end_among_thousands_of_sequences_is_looked_over_in_passing():
+    """4,096 sequences of eight tokens, one of whose ends goes back by sixteen: two others' rows are owned
+    twice, all are written, and the call stays a call of milliseconds."""
+    B, n, P, D = 4096, 8, 16, 64
+    ends = np.arange(B + 1, dtype=np.int32) * n
+    ends[2000] -= 16
+    sh = C.ChunkShape(B, 1, 1, D, P, B * n, 24, 32, 2, 2 * B)
+    g = torch.Generator().manual_seed(120)
+    x = torch.randn(B * n, 3, D, generator=g).to(torch.bfloat16).cuda()
+    table = torch.arange(2 * B, dtype=torch.int32, device="cuda").view(B, 2)
+    cu, kv = torch.from_numpy(ends).cuda(), torch.full((B,), 24, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.full((2 * B, 1, P, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.full((B * n, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    times = []
+    for _ in range(3):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        C.cosa_chunk_write(sh, None, x[:, :1], x[:, 1:2], x[:, 2:], None, None, cu, kv, table, q, kp, vp)
+        e[1].record()
+        torch.cuda.synchronize()
+        times.append(e[0].elapsed_time(e[1]))
+        assert C.cosa_get_status() == 1
+    assert min(times) < 500
+    want = torch.full((B, 2 * P, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    for b in range(B):
+        m = int(ends[b + 1] - ends[b])
+        if m > 0:
+            want[b, 24 - m:24] = x[int(ends[b]):int(ends[b + 1]), 1]
+    assert torch.equal(kp.view(B, 2 * P, D), want)
+    assert torch.equal(q, x[:, :1])
+
